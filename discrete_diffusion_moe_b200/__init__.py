@@ -20,6 +20,9 @@ DG_OK, DG_ERR_INVALID_ARG, DG_ERR_CUDA, DG_ERR_WORKSPACE, DG_ERR_TIMEOUT, DG_ERR
 DG_LOCK_PROB, DG_LOCK_ENTROPY_CUMSUM = 0, 1
 DG_DECODE_DEFER_APPEND = 1
 
+DG_BF16, DG_F16, DG_F32 = range(3)
+DG_ACT_NONE, DG_ACT_SWIGLU, DG_ACT_SWIGLU_INTERLEAVED = range(3)
+
 # size of the library's fixed split-KV scratch array (dg_attention_static_scratch)
 DG_ATTN_STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -89,6 +92,7 @@ def _load():
             "(nvcc, sm_100a); this package has no CPU fallback")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, I32, U64, F = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_uint64, ctypes.c_float
+    I64 = ctypes.c_int64
     cfgp = ctypes.POINTER(dg_model_config)
     sig = {
         "dg_last_error": (ctypes.c_char_p, []),
@@ -128,6 +132,10 @@ def _load():
         "dg_router_probe": (I32, [P, I32, P, I32, P, P]),
         "dg_ar_step": (I32, [P, ctypes.POINTER(dg_kv), P, F, U64, P, P, P, P]),
         "dg_attention_static_scratch": (I32, [P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P]),
+        "dg_fp8_quantize": (I32, [P, I32, I64, I64, P, I32, I64, I64, P, I64, P, I64, P]),
+        "dg_fp8_quantize_blocks": (I32, [P, I32, I64, I64, I64, I64, P, I64, P, P]),
+        "dg_fp8_gemm": (I32, [P, I64, P, I64, P, I64, P, I64, I64, I64, P, P, I32, I64, P]),
+        "dg_fp8_grouped_gemm": (I32, [P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, P, P, I32, I64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -221,3 +229,4 @@ def dg_test_grouped_gemm(d_a, rows_per_group, n_groups, d_b, n_rows, K, d_off, d
 
 
 from .runtime import Model, KVCache, Canvas, StepOutputs, sampler_config, model_config  # noqa: E402,F401
+from .fp8 import fp8_gemm, fp8_grouped_gemm, fp8_quantize, fp8_quantize_blocks  # noqa: E402,F401

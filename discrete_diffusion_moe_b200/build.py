@@ -14,11 +14,12 @@ LIB = os.path.join(PKG, "libdg.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
-CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared"]
+CFLAGS = ["-O3", "-t", "4", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared"]
 
 
 def sources():
-    return [os.path.join(PKG, "csrc", "dg_api.cu"), os.path.join(ROOT, "synth", "synth_device.cu")]
+    return [os.path.join(PKG, "csrc", "dg_api.cu"), os.path.join(PKG, "csrc", "fp8_api.cu"),
+            os.path.join(ROOT, "synth", "synth_device.cu")]
 
 
 def deps():

@@ -24,6 +24,7 @@
 #include "epilogues.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_tc.cuh"
+#include "host.cuh"
 #include "moe_pair.cuh"
 #include "kernels.cuh"
 
@@ -33,26 +34,13 @@ using namespace dg;
 // errors
 static thread_local char g_err[512] = "";
 
-static dg_status fail(dg_status s, const char* fmt, ...) {
+dg_status dg::fail(dg_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
   return s;
 }
-
-#define DG_CUDA(call)                                                                        \
-  do {                                                                                       \
-    cudaError_t e_ = (call);                                                                 \
-    if (e_ != cudaSuccess) return fail(DG_ERR_CUDA, "%s: %s (%s:%d)", #call,                \
-                                       cudaGetErrorString(e_), __FILE__, __LINE__);          \
-  } while (0)
-
-#define DG_TRY(expr)                  \
-  do {                                \
-    dg_status s_ = (expr);            \
-    if (s_ != DG_OK) return s_;       \
-  } while (0)
 
 extern "C" const char* dg_last_error(void) { return g_err; }
 
@@ -65,15 +53,6 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
-// One kernel launch.  With DG_PDL (programmatic dependent launch) its CTAs
-// may be scheduled while the stream's previous kernel finishes: every kernel
-// of the library waits (griddepcontrol.wait) before it touches memory that
-// another kernel writes, so only its launch latency and its own set-up
-// (barriers, tensor memory, tensor-map prefetch) overlap the predecessor's
-// tail.  Optional cluster shape and cluster scheduling policy.
-#ifndef DG_PDL
-#define DG_PDL 1
-#endif
 // 1: the QKV and output projections run on CTA pairs (each CTA of a pair
 // copies half of the unit's token rows), with the same k splits and partials
 #ifndef DG_PROJ_PAIR
@@ -96,41 +75,6 @@ struct NvtxRange {
 #ifndef DG_GROUPED_BN
 #define DG_GROUPED_BN 0
 #endif
-struct Launch {
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute at[3];
-  Launch(dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool pdl = DG_PDL) {
-    lc.gridDim = grid;
-    lc.blockDim = block;
-    lc.dynamicSmemBytes = smem;
-    lc.stream = st;
-    lc.attrs = at;
-    if (pdl) {
-      at[lc.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      at[lc.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-      ++lc.numAttrs;
-    }
-  }
-  Launch& cluster(unsigned x, unsigned y, unsigned z) {
-    at[lc.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    at[lc.numAttrs].val.clusterDim.x = x;
-    at[lc.numAttrs].val.clusterDim.y = y;
-    at[lc.numAttrs].val.clusterDim.z = z;
-    ++lc.numAttrs;
-    return *this;
-  }
-  Launch& policy(cudaClusterSchedulingPolicy pol) {
-    at[lc.numAttrs].id = cudaLaunchAttributeClusterSchedulingPolicyPreference;
-    at[lc.numAttrs].val.clusterSchedulingPolicyPreference = pol;
-    ++lc.numAttrs;
-    return *this;
-  }
-  template <typename... KArgs, typename... Args>
-  cudaError_t operator()(void (*k)(KArgs...), Args&&... args) {
-    return cudaLaunchKernelEx(&lc, k, std::forward<Args>(args)...);
-  }
-};
-
 // ============================================================================
 // configuration checks and layouts
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -328,24 +272,7 @@ WsLayout ws_layout(const dg_model_config& c, int batch, int num_sms, int prefill
 }
 
 // ---------------------------------------------------------------------------
-// TMA tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                  CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeTiledFn)p;
-  }
-  return fn;
-}
-
+// TMA tensor maps (encode_fn: host.cuh)
 // K-major bf16 matrix [rows, K] (row stride K elements), box 64 x box_rows,
 // 128-byte swizzle.
 dg_status make_tmap(CUtensorMap* m, const void* base, long long K, long long rows, int box_rows) {
@@ -428,28 +355,6 @@ dg_status make_bop_half(BOperand* b, const void* base, long long K, long long ro
     DG_TRY(make_tmap(&b->maps.m[i], base, K, rows, b->rows[i]));
   }
   return DG_OK;
-}
-
-// cudaFuncSetAttribute applies to the kernel in the current device's context:
-// set each (kernel, device) once, the first time a launch on that device
-// needs it.
-dg_status set_smem_attr(const void* fn, int bytes, bool max_carveout) {
-  static std::mutex mu;
-  static std::set<std::pair<const void*, int>> done;
-  int dev = 0;
-  DG_CUDA(cudaGetDevice(&dev));
-  std::lock_guard<std::mutex> lock(mu);
-  if (done.count({fn, dev})) return DG_OK;
-  DG_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  if (max_carveout) DG_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100));
-  done.insert({fn, dev});
-  return DG_OK;
-}
-
-int device_sms() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n;
 }
 
 template <class Epi>

@@ -1,0 +1,191 @@
+// fp8_api.cu - host side of the 8-bit block-scaled operators of include/dg.h:
+// argument checks, choice of kernel and launches.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/dg.h"
+#include "fp8_quant.cuh"
+#include "fp8_small.cuh"
+#include "host.cuh"
+
+using namespace dg;
+
+namespace {
+
+constexpr long long kMaxDim = 2147483647ll;
+constexpr int kFp8MaxGroups = 1024;
+
+size_t dtype_bytes(int dt) { return dt == DG_F32 ? 4 : 2; }
+bool dtype_ok(int dt) { return dt == DG_BF16 || dt == DG_F16 || dt == DG_F32; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+template <class T, int ACT>
+dg_status launch_quant_rows(const QuantRowsParams& p, bool vec, cudaStream_t st) {
+  const long long tasks = (long long)p.rows * p.KB;
+  const long long per_cta = (long long)kQuantThreads / 32 * 2 * kQuantTasks;
+  const dim3 grid((unsigned)ceil_div(tasks, per_cta));
+  if (vec) DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, true>, p));
+  else     DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, false>, p));
+  return DG_OK;
+}
+
+template <class T>
+dg_status launch_quant_rows(const QuantRowsParams& p, int act, bool vec, cudaStream_t st) {
+  switch (act) {
+    case DG_ACT_NONE: return launch_quant_rows<T, kActNone>(p, vec, st);
+    case DG_ACT_SWIGLU: return launch_quant_rows<T, kActSwiglu>(p, vec, st);
+    default: return launch_quant_rows<T, kActSwigluInterleaved>(p, vec, st);
+  }
+}
+
+template <class T>
+dg_status launch_quant_blocks(const QuantBlocksParams& p, long long blocks, bool vec, cudaStream_t st) {
+  if (vec) DG_CUDA(Launch(dim3((unsigned)blocks), dim3(256), 0, st)(quant_blocks_kernel<T, true>, p));
+  else     DG_CUDA(Launch(dim3((unsigned)blocks), dim3(256), 0, st)(quant_blocks_kernel<T, false>, p));
+  return DG_OK;
+}
+
+template <class TO>
+dg_status launch_small(const Fp8GemmParams& p, cudaStream_t st) {
+  const unsigned slots = p.off ? (unsigned)std::min(p.G, p.M) : 1u;
+  const dim3 grid((unsigned)ceil_div(p.N, 16), slots);
+  if (p.M <= 8) DG_CUDA(Launch(grid, dim3(32 * kSmallWarps), 0, st)(fp8_small_kernel<1, 1, 3, TO>, p));
+  else          DG_CUDA(Launch(grid, dim3(32 * kSmallWarps), 0, st)(fp8_small_kernel<1, 2, 2, TO>, p));
+  return DG_OK;
+}
+
+dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, cudaStream_t st) {
+  switch (out_dtype) {
+    case DG_BF16: return launch_small<__nv_bfloat16>(p, st);
+    case DG_F16: return launch_small<__half>(p, st);
+    case DG_F32: return launch_small<float>(p, st);
+    default: return fail(DG_ERR_INVALID_ARG, "%s: output type %d", who, out_dtype);
+  }
+}
+
+// Checks shared by the dense and the grouped product; fills `p`.
+dg_status check_product(const char* who, const uint8_t* a, int64_t lda, const float* sa, int64_t lds,
+                        const uint8_t* b, int64_t ldb, const float* sb, const int32_t* off, int64_t G, int64_t M,
+                        int64_t N, int64_t K, const float* row_w, void* out, int32_t out_dtype, int64_t ldo,
+                        Fp8GemmParams* p) {
+  if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return fail(DG_ERR_INVALID_ARG, "%s: sizes %lld x %lld x %lld", who, (long long)M, (long long)N, (long long)K);
+  if (!dtype_ok(out_dtype)) return fail(DG_ERR_INVALID_ARG, "%s: output type %d", who, (int)out_dtype);
+  if (G < 1 || G > kFp8MaxGroups) return fail(DG_ERR_INVALID_ARG, "%s: %lld groups (1..%d)", who, (long long)G, kFp8MaxGroups);
+  if (G * N > kMaxDim) return fail(DG_ERR_INVALID_ARG, "%s: groups x N exceeds 2^31 - 1", who);
+  if (lda < K || lda % 16 || ldb < K || ldb % 16)
+    return fail(DG_ERR_INVALID_ARG, "%s: row pitches %lld, %lld of the codes (multiples of 16, at least K = %lld)", who,
+                (long long)lda, (long long)ldb, (long long)K);
+  if (lds < M || ldo < N)
+    return fail(DG_ERR_INVALID_ARG, "%s: pitch %lld of the row scales (at least M), %lld of the output (at least N)", who,
+                (long long)lds, (long long)ldo);
+  if (M == 0) { *p = Fp8GemmParams{}; return DG_OK; }
+  if (!a || !sa || !b || !sb || !out) return fail(DG_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (!aligned(a, 16) || !aligned(b, 16)) return fail(DG_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned", who);
+  const size_t osz = dtype_bytes(out_dtype);
+  if (!aligned(sa, 4) || !aligned(sb, 4) || !aligned(off, 4) || !aligned(row_w, 4) || !aligned(out, osz))
+    return fail(DG_ERR_INVALID_ARG, "%s: misaligned pointer", who);
+  Fp8GemmParams q{};
+  q.a = a; q.lda = lda; q.sa = sa; q.lds = lds;
+  q.b = b; q.ldb = ldb; q.sb = sb;
+  q.row_w = row_w; q.off = off;
+  q.out = out; q.ldo = ldo;
+  q.M = (int)M; q.N = (int)N; q.K = (int)K;
+  q.KB = (int)ceil_div(K, kFp8Block);
+  q.NB = (int)ceil_div(N, kFp8Block);
+  q.G = (int)G;
+  q.vec_out = aligned(out, 16) && (ldo * (long long)osz) % 16 == 0;
+  *p = q;
+  return DG_OK;
+}
+
+}  // namespace
+
+extern "C" dg_status dg_fp8_quantize(const void* d_x, int32_t dtype, int64_t ldx, int64_t x_rows,
+                                     const int32_t* d_index, int32_t act, int64_t rows, int64_t cols, uint8_t* d_q,
+                                     int64_t ldq, float* d_scale, int64_t lds, void* stream) {
+  if (!dtype_ok(dtype)) return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: input type %d", (int)dtype);
+  if (act < DG_ACT_NONE || act > DG_ACT_SWIGLU_INTERLEAVED)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: activation %d", (int)act);
+  if (rows < 0 || cols < 1 || x_rows < 0 || rows > kMaxDim || x_rows > kMaxDim || cols > kMaxDim / 2)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: sizes %lld (of %lld) x %lld", (long long)rows, (long long)x_rows,
+                (long long)cols);
+  const long long in_cols = act == DG_ACT_NONE ? cols : 2 * cols;
+  if (ldx < in_cols || ldq < cols || ldq % 16 || lds < rows)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: pitches %lld of x, %lld of the codes (a multiple of 16), %lld of the scales",
+                (long long)ldx, (long long)ldq, (long long)lds);
+  if (!d_index && x_rows < rows)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: %lld rows of x for %lld output rows", (long long)x_rows, (long long)rows);
+  if (rows == 0) return DG_OK;
+  if ((!d_x && x_rows > 0) || !d_q || !d_scale) return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: null pointer");
+  const size_t sz = dtype_bytes(dtype);
+  if (!aligned(d_x, sz) || !aligned(d_q, 16) || !aligned(d_scale, 4) || !aligned(d_index, 4))
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: misaligned pointer (codes: 16 bytes)");
+  QuantRowsParams p{};
+  p.x = d_x; p.ldx = ldx; p.index = d_index; p.x_rows = x_rows;
+  p.q = d_q; p.ldq = ldq; p.scale = d_scale; p.lds = lds;
+  p.rows = (int)rows; p.K = (int)cols; p.KB = (int)ceil_div(cols, kFp8Block);
+  if (ceil_div((long long)p.rows * p.KB, (long long)kQuantThreads / 32 * 2 * kQuantTasks) > kMaxDim)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: too many blocks");
+  const bool vec = cols % 8 == 0 && aligned(d_x, 16) && (ldx * (long long)sz) % 16 == 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  switch (dtype) {
+    case DG_BF16: return launch_quant_rows<__nv_bfloat16>(p, act, vec, st);
+    case DG_F16: return launch_quant_rows<__half>(p, act, vec, st);
+    default: return launch_quant_rows<float>(p, act, vec, st);
+  }
+}
+
+extern "C" dg_status dg_fp8_quantize_blocks(const void* d_w, int32_t dtype, int64_t ldw, int64_t groups, int64_t rows,
+                                            int64_t cols, uint8_t* d_q, int64_t ldq, float* d_scale, void* stream) {
+  if (!dtype_ok(dtype)) return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize_blocks: input type %d", (int)dtype);
+  if (groups < 0 || rows < 1 || cols < 1 || groups > kMaxDim || rows > kMaxDim || cols > kMaxDim)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize_blocks: sizes %lld x %lld x %lld", (long long)groups, (long long)rows,
+                (long long)cols);
+  if (ldw < cols || ldq < cols || ldq % 16)
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize_blocks: pitches %lld of w, %lld of the codes (a multiple of 16)",
+                (long long)ldw, (long long)ldq);
+  if (groups == 0) return DG_OK;
+  if (!d_w || !d_q || !d_scale) return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize_blocks: null pointer");
+  const size_t sz = dtype_bytes(dtype);
+  if (!aligned(d_w, sz) || !aligned(d_q, 16) || !aligned(d_scale, 4))
+    return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize_blocks: misaligned pointer (codes: 16 bytes)");
+  QuantBlocksParams p{};
+  p.w = d_w; p.ldw = ldw; p.q = d_q; p.ldq = ldq; p.scale = d_scale;
+  p.N = (int)rows; p.K = (int)cols;
+  p.NB = (int)ceil_div(rows, kFp8Block); p.KB = (int)ceil_div(cols, kFp8Block);
+  const double blocks_d = (double)groups * p.NB * p.KB;
+  if (blocks_d > (double)kMaxDim) return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize_blocks: too many blocks");
+  const long long blocks = (long long)groups * p.NB * p.KB;
+  const bool vec = cols % 8 == 0 && aligned(d_w, 16) && (ldw * (long long)sz) % 16 == 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  switch (dtype) {
+    case DG_BF16: return launch_quant_blocks<__nv_bfloat16>(p, blocks, vec, st);
+    case DG_F16: return launch_quant_blocks<__half>(p, blocks, vec, st);
+    default: return launch_quant_blocks<float>(p, blocks, vec, st);
+  }
+}
+
+extern "C" dg_status dg_fp8_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds,
+                                 const uint8_t* d_b, int64_t ldb, const float* d_b_scale, int64_t M, int64_t N, int64_t K,
+                                 const float* d_row_weight, void* d_out, int32_t out_dtype, int64_t ldo, void* stream) {
+  Fp8GemmParams p;
+  DG_TRY(check_product("dg_fp8_gemm", d_a, lda, d_a_scale, lds, d_b, ldb, d_b_scale, nullptr, 1, M, N, K, d_row_weight,
+                       d_out, out_dtype, ldo, &p));
+  if (M == 0) return DG_OK;
+  return product("dg_fp8_gemm", p, out_dtype, (cudaStream_t)stream);
+}
+
+extern "C" dg_status dg_fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds,
+                                         const uint8_t* d_b, int64_t ldb, const float* d_b_scale, const int32_t* d_off,
+                                         int64_t groups, int64_t M, int64_t N, int64_t K, const float* d_row_weight,
+                                         void* d_out, int32_t out_dtype, int64_t ldo, void* stream) {
+  Fp8GemmParams p;
+  if (!d_off) return fail(DG_ERR_INVALID_ARG, "dg_fp8_grouped_gemm: null offsets");
+  DG_TRY(check_product("dg_fp8_grouped_gemm", d_a, lda, d_a_scale, lds, d_b, ldb, d_b_scale, d_off, groups, M, N, K,
+                       d_row_weight, d_out, out_dtype, ldo, &p));
+  if (M == 0) return DG_OK;
+  return product("dg_fp8_grouped_gemm", p, out_dtype, (cudaStream_t)stream);
+}

@@ -1,0 +1,286 @@
+// fp8_quant.cuh - quantisers to e4m3 with one fp32 scale for each block of 128:
+// rows of activations (one scale per row and 128 columns) and weight matrices
+// (one scale per 128 x 128 block).
+//
+// With a = max |x| of the block, raised to at least 2^-100 (so that 448 / a
+// and a / 448 are normal numbers, and a block of zeros needs no case of its
+// own):
+//   scale = a / 448,   q = e4m3(x * (448 / a))
+// the quotients and the product in fp32 (each rounded to nearest), the code
+// rounded to nearest even and held to +-448.  The product with 448 / a instead
+// of a quotient by the scale saves a division per element; it moves x / scale
+// by at most 2^-23 of its value, 2^-19 of a code's rounding step.  A block that
+// holds a NaN or an infinity gets the scale NaN and codes 0: every product it
+// enters is NaN.
+//
+// Both are bound by HBM: one read of x, one write of the codes.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace dg {
+
+constexpr int kFp8Block = 128;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kFp8AmaxMin = 7.888609052210118e-31f;  // 2^-100
+
+enum { kActNone = 0, kActSwiglu = 1, kActSwigluInterleaved = 2 };
+
+// ---- loads -------------------------------------------------------------------
+__device__ __forceinline__ float elem_f32(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
+__device__ __forceinline__ float elem_f32(const __half* p) { return __half2float(__ldg(p)); }
+__device__ __forceinline__ float elem_f32(const float* p) { return __ldg(p); }
+
+// eight consecutive elements (16-byte aligned) as raw words, and their values
+template <class T>
+struct Raw8 {
+  static constexpr int kVecs = (int)sizeof(T) / 2;  // 16-byte vectors
+  uint4 r[kVecs];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) r[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ float get(int i) const;
+};
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
+}
+template <>
+__device__ __forceinline__ float Raw8<__nv_bfloat16>::get(int i) const {
+  const uint32_t w = word_of(r[0], i >> 1);
+  return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+}
+template <>
+__device__ __forceinline__ float Raw8<__half>::get(int i) const {
+  const uint32_t w = word_of(r[0], i >> 1);
+  return __half2float(__ushort_as_half((unsigned short)((i & 1) ? (w >> 16) : (w & 0xffffu))));
+}
+template <>
+__device__ __forceinline__ float Raw8<float>::get(int i) const {
+  return __uint_as_float(word_of(r[i >> 2], i & 3));
+}
+
+// silu(g) * u.  __expf and __fdividef: a few 2^-23 of relative error (the
+// exponent's rounding adds |g| 2^-24), far below the code's 2^-4 step; for
+// e^-g above 2^126 the quotient is 0, as silu's own limit.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// ---- block scale and codes ------------------------------------------------------
+struct BlockScale {
+  float scale, inv;
+};
+// amax_bits: the largest bit pattern of |x| of the block; patterns from
+// infinity up (infinities and NaNs) compare above every finite one
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return {__uint_as_float(0x7fffffffu), 0.f};
+  const float a = fmaxf(__uint_as_float(amax_bits), kFp8AmaxMin);
+  return {__fdiv_rn(a, kE4m3Max), __fdiv_rn(kE4m3Max, a)};
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// ---- rows ---------------------------------------------------------------------------
+struct QuantRowsParams {
+  const void* x;
+  long long ldx;          // elements between rows of x
+  const int32_t* index;   // optional [rows]: the row of x each output row takes
+  long long x_rows;       // rows of x; an index outside [0, x_rows) reads as a row of zeros
+  uint8_t* q;
+  long long ldq;
+  float* scale;           // [KB][lds]
+  long long lds;
+  int rows, K, KB;
+};
+
+// Half a warp takes one (row, block of 128 columns): eight elements per lane, so
+// a row's block is one 256-byte load of bf16 and the maximum takes four
+// shuffles.  A warp takes 2 * kQuantTasks consecutive tasks and issues all
+// their loads first: the kernel is latency-bound otherwise (one load in flight
+// per lane reached about half the bandwidth).  kVec: 16-byte loads and 8-byte
+// stores (every row of x 16-byte aligned and K a multiple of 8); otherwise lane
+// l takes elements l, l + 16, ... one by one.
+constexpr int kQuantTasks = 4;
+constexpr int kQuantThreads = 256;
+
+template <class T, int ACT, bool kVec>
+__global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantRowsParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const long long warp = (long long)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
+  const long long tasks = (long long)p.rows * p.KB;
+  const long long first = warp * (2 * kQuantTasks) + (lane >> 4);
+  constexpr int kIn = ACT == kActNone ? 1 : 2;
+  const T* const x = static_cast<const T*>(p.x);
+
+  int row[kQuantTasks], kb[kQuantTasks];
+  Raw8<T> raw[kVec ? kQuantTasks : 1][kIn];
+  float v[kQuantTasks][8];
+#pragma unroll
+  for (int u = 0; u < kQuantTasks; ++u) {
+    const long long t = first + 2 * u;
+    row[u] = t < tasks ? (int)(t / p.KB) : -1;
+    kb[u] = t < tasks ? (int)(t - (long long)row[u] * p.KB) : 0;
+    long long src = row[u];
+    if (p.index && row[u] >= 0) {
+      src = __ldg(p.index + row[u]);
+      if (src >= p.x_rows) src = -1;
+    }
+    const T* xr = x + (src < 0 ? 0 : src) * p.ldx;
+    if constexpr (kVec) {
+      const int k0 = kb[u] * kFp8Block + l * 8;
+      const bool on = src >= 0 && k0 < p.K;  // K is a multiple of 8: all eight or none
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) raw[u][i].zero();
+      if (on) {
+        if constexpr (ACT == kActNone) {
+          raw[u][0].load(xr + k0);
+        } else if constexpr (ACT == kActSwiglu) {
+          raw[u][0].load(xr + k0);
+          raw[u][1].load(xr + p.K + k0);
+        } else {
+          raw[u][0].load(xr + 2 * (long long)k0);
+          raw[u][1].load(xr + 2 * (long long)k0 + 8);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = kb[u] * kFp8Block + i * 16 + l;
+        const bool on = src >= 0 && k < p.K;
+        if constexpr (ACT == kActNone) {
+          v[u][i] = on ? elem_f32(xr + k) : 0.f;
+        } else {
+          const T* gp = ACT == kActSwiglu ? xr + k : xr + 2 * (long long)k;
+          const T* up = ACT == kActSwiglu ? xr + p.K + k : gp + 1;
+          v[u][i] = on ? swiglu(elem_f32(gp), elem_f32(up)) : 0.f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kQuantTasks; ++u) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (ACT == kActNone) v[u][i] = raw[u][0].get(i);
+        else if constexpr (ACT == kActSwiglu) v[u][i] = swiglu(raw[u][0].get(i), raw[u][1].get(i));
+        else v[u][i] = swiglu(raw[u][i >> 2].get((2 * i) & 7), raw[u][i >> 2].get(((2 * i) & 7) + 1));
+      }
+    }
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[u][i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (row[u] < 0) continue;
+    const BlockScale s = block_scale(m);
+    uint8_t* const qr = p.q + (long long)row[u] * p.ldq + kb[u] * kFp8Block;
+    uint32_t lo = 0u, hi = 0u;
+    if (s.inv != 0.f) {  // codes 0 where the scale is NaN
+      lo = codes4(v[u][0] * s.inv, v[u][1] * s.inv, v[u][2] * s.inv, v[u][3] * s.inv);
+      hi = codes4(v[u][4] * s.inv, v[u][5] * s.inv, v[u][6] * s.inv, v[u][7] * s.inv);
+    }
+    if constexpr (kVec) {
+      if (kb[u] * kFp8Block + l * 8 < p.K) *reinterpret_cast<uint2*>(qr + l * 8) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (kb[u] * kFp8Block + i * 16 + l < p.K)
+          qr[i * 16 + l] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    }
+    if (l == 0) p.scale[(long long)kb[u] * p.lds + row[u]] = s.scale;
+  }
+}
+
+// ---- 128 x 128 blocks -------------------------------------------------------------------
+struct QuantBlocksParams {
+  const void* w;
+  long long ldw;    // elements between rows; a group's rows follow the previous group's
+  uint8_t* q;
+  long long ldq;
+  float* scale;     // [G][NB][KB]
+  int N, K, NB, KB;
+};
+
+// One CTA per block: 256 threads hold its 16384 elements in registers (eight
+// vectors of eight; all loads in flight together), take the maximum over the
+// CTA and write the codes, so x is read once.
+template <class T, bool kVec>
+__global__ void __launch_bounds__(256) quant_blocks_kernel(const QuantBlocksParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  __shared__ uint32_t s_max[8];
+  const int kb = (int)(blockIdx.x % (unsigned)p.KB);
+  const unsigned rest = blockIdx.x / (unsigned)p.KB;
+  const int nb = (int)(rest % (unsigned)p.NB);
+  const long long g = rest / (unsigned)p.NB;
+  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const long long row_base = g * p.N;
+  const T* const w = static_cast<const T*>(p.w);
+
+  Raw8<T> raw[kVec ? 8 : 1];
+  float v[kVec ? 1 : 8][8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int n = nb * kFp8Block + u * 16 + r0;
+    const T* wr = w + (row_base + n) * p.ldw;
+    if constexpr (kVec) {
+      raw[u].zero();
+      const int k = kb * kFp8Block + c * 8;
+      if (n < p.N && k < p.K) raw[u].load(wr + k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = kb * kFp8Block + i * 16 + c;
+        v[u][i] = (n < p.N && k < p.K) ? elem_f32(wr + k) : 0.f;
+      }
+    }
+  }
+  auto val = [&](int u, int i) -> float {
+    if constexpr (kVec) return raw[u].get(i);
+    else return v[u][i];
+  };
+  uint32_t m = 0u;
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(val(u, i)));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, s_max[i]);
+  const BlockScale s = block_scale(m);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int n = nb * kFp8Block + u * 16 + r0;
+    if (n >= p.N) continue;
+    uint8_t* const qr = p.q + (row_base + n) * p.ldq + kb * kFp8Block;
+    uint32_t lo = 0u, hi = 0u;
+    if (s.inv != 0.f) {
+      lo = codes4(val(u, 0) * s.inv, val(u, 1) * s.inv, val(u, 2) * s.inv, val(u, 3) * s.inv);
+      hi = codes4(val(u, 4) * s.inv, val(u, 5) * s.inv, val(u, 6) * s.inv, val(u, 7) * s.inv);
+    }
+    if constexpr (kVec) {
+      if (kb * kFp8Block + c * 8 < p.K) *reinterpret_cast<uint2*>(qr + c * 8) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (kb * kFp8Block + i * 16 + c < p.K) qr[i * 16 + c] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+    }
+  }
+  if (threadIdx.x == 0) p.scale[blockIdx.x] = s.scale;
+}
+
+}  // namespace dg

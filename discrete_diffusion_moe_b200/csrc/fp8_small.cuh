@@ -1,0 +1,215 @@
+// fp8_small.cuh - the block-scaled e4m3 product for few rows (single tokens,
+// experts with a handful of tokens):
+//
+//   D[m, n] = w[m] * sum_kb sa[kb, m] * sb[n / 128, kb] * sum_{k in block kb} A[m, k] * B[n, k]
+//
+// A: activation codes [M, K], B: weight codes [N, K] (or [G, N, K] with the rows
+// of A split among the groups).  The time is the one read of B.
+//
+// mma.sync m16n8k32 with 16 weight rows as its M side and 8 tokens as its N
+// side: a tcgen05 tile would spend 128 rows on one token, and here the weights
+// go from global memory to registers without a stop in shared memory.  The
+// order of k inside a block is free as long as A and B agree, so lane (g, t)
+// of a warp takes the 32 consecutive bytes [32 t, 32 t + 32) of its rows: two
+// 16-byte loads per row, four products per block.  The eight warps of a CTA
+// share its features and take every eighth block of K each: all of a CTA's
+// loads are in flight together.  Their fp32 partial sums meet in shared memory
+// in the order of the warps (the result does not depend on timing).
+#pragma once
+
+#include "common.cuh"
+#include "fp8_quant.cuh"
+
+namespace dg {
+
+// Rows [row0, row1) of a group, held inside [0, M) whatever the offsets say.
+struct RowRange {
+  int row0, row1;
+};
+__device__ __forceinline__ RowRange group_rows(const int32_t* off, int g, int M) {
+  const int r0 = min(max(__ldg(off + g), 0), M);
+  return {r0, min(max(__ldg(off + g + 1), r0), M)};
+}
+
+struct Fp8GemmParams {
+  const uint8_t* a;
+  long long lda;
+  const float* sa;        // [KB][lds]
+  long long lds;
+  const uint8_t* b;       // [G][N] rows of ldb bytes
+  long long ldb;
+  const float* sb;        // [G][NB][KB]
+  const float* row_w;     // optional [M]
+  const int32_t* off;     // grouped: [G + 1]; null: one group of all rows
+  void* out;
+  long long ldo;
+  int M, N, K, KB, NB, G;
+  int vec_out;            // rows of the output start on 16-byte boundaries
+};
+
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_out(__half* p, float v) { *p = __float2half_rn(v); }
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p));
+  return v;
+}
+// the first n bytes of a word
+__device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int n) {
+  return n >= 4 ? w : (n <= 0 ? 0u : (w & ((1u << (8 * n)) - 1u)));
+}
+// 32 consecutive codes of one row from column k0 on; columns from K on read as 0.
+// A 16-byte word is read only where its first byte is inside the row, so the
+// reads stay within the row's 16-byte pitch.
+template <bool kStream>
+__device__ __forceinline__ void load_codes32(uint32_t (&w)[8], const uint8_t* row, int k0, int K, bool on) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (on && k0 + 16 * h < K) {
+      if constexpr (kStream) v = ld_stream(row + k0 + 16 * h);
+      else v = __ldg(reinterpret_cast<const uint4*>(row + k0 + 16 * h));
+    }
+    w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
+  }
+}
+
+constexpr int kSmallWarps = 8;
+
+// kMT 16-feature tiles and kNT 8-token tiles per CTA, kKU blocks of K loaded
+// together by each warp.
+template <int kMT, int kNT, int kKU, class TO>
+__global__ void __launch_bounds__(32 * kSmallWarps) fp8_small_kernel(const Fp8GemmParams p) {
+  constexpr int kFeat = 16 * kMT, kTok = 8 * kNT;
+  __shared__ float red[kSmallWarps][kTok][kFeat + 1];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kFeat;
+
+  // the blockIdx.y-th group that has rows
+  int grp = 0, row0 = 0, row1 = p.M;
+  if (p.off) {
+    int want = (int)blockIdx.y;
+    grp = -1;
+    for (int base = 0; base < p.G; base += 32) {
+      RowRange r{0, 0};
+      if (base + lane < p.G) r = group_rows(p.off, base + lane, p.M);
+      const unsigned has = __ballot_sync(0xffffffffu, r.row1 > r.row0);
+      if (want < __popc(has)) {
+        const bool mine = r.row1 > r.row0 && __popc(has & ((1u << lane) - 1u)) == want;
+        const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        grp = base + src;
+        row0 = __shfl_sync(0xffffffffu, r.row0, src);
+        row1 = __shfl_sync(0xffffffffu, r.row1, src);
+        break;
+      }
+      want -= __popc(has);
+    }
+    if (grp < 0) return;  // the same for every warp of the CTA
+  }
+  const uint8_t* const b = p.b + (long long)grp * p.N * p.ldb;
+  const float* const sb = p.sb + ((long long)grp * p.NB + n0 / kFp8Block) * p.KB;
+
+  for (int m0 = row0; m0 < row1; m0 += kTok) {
+    float acc[kMT][kNT][4];
+#pragma unroll
+    for (int i = 0; i < kMT; ++i)
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+
+    for (int kb0 = warp; kb0 < p.KB; kb0 += kSmallWarps * kKU) {
+      uint32_t wb[kKU][kMT][2][8], wa[kKU][kNT][8];
+      float sc[kKU][kNT][2];
+#pragma unroll
+      for (int q = 0; q < kKU; ++q) {
+        const int kb = kb0 + q * kSmallWarps;
+        const int k0 = kb * kFp8Block + 32 * t;
+        const bool on = kb < p.KB;
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = n0 + 16 * i + 8 * h + g;
+            load_codes32<true>(wb[q][i][h], b + (long long)n * p.ldb, k0, p.K, on && n < p.N);
+          }
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+          const int m = m0 + 8 * j + g;
+          load_codes32<false>(wa[q][j], p.a + (long long)m * p.lda, k0, p.K, on && m < row1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int mc = m0 + 8 * j + 2 * t + e;
+            sc[q][j][e] = on && mc < row1 ? __ldg(p.sa + (long long)kb * p.lds + mc) * __ldg(sb + kb) : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kKU; ++q) {
+        const int kb = kb0 + q * kSmallWarps;
+        if (kb >= p.KB) break;
+        if ((kb + 1) * kFp8Block > p.K) {
+          // K ends inside this block: what lies behind it in the rows may be anything
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            const int left = p.K - (kb * kFp8Block + 32 * t + 4 * w);
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) {
+              wb[q][i][0][w] = keep_bytes(wb[q][i][0][w], left);
+              wb[q][i][1][w] = keep_bytes(wb[q][i][1][w], left);
+            }
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) wa[q][j][w] = keep_bytes(wa[q][j][w], left);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              mma_e4m3(c, wb[q][i][0][2 * s], wb[q][i][1][2 * s], wb[q][i][0][2 * s + 1], wb[q][i][1][2 * s + 1],
+                       wa[q][j][2 * s], wa[q][j][2 * s + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], sc[q][j][e & 1], acc[i][j][e]);
+          }
+      }
+    }
+    // accumulator (i, j): features 16 i + g (e 0, 1) and + 8 (e 2, 3), tokens 8 j + 2 t + (e & 1)
+#pragma unroll
+    for (int i = 0; i < kMT; ++i)
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          red[warp][8 * j + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] = acc[i][j][e];
+    __syncthreads();
+    for (int o = threadIdx.x; o < kTok * kFeat; o += 32 * kSmallWarps) {
+      const int tok = o / kFeat, f = o - tok * kFeat;
+      const int m = m0 + tok, n = n0 + f;
+      if (m < row1 && n < p.N) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) s += red[w][tok][f];
+        if (p.row_w) s *= __ldg(p.row_w + m);
+        store_out(static_cast<TO*>(p.out) + (long long)m * p.ldo + n, s);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace dg

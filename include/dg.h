@@ -372,6 +372,68 @@ dg_status dg_attention_static_scratch(const uint16_t* d_q, const uint16_t* d_k, 
                                       int32_t Hq, int32_t Hkv, int32_t hd, int32_t causal, int32_t splits,
                                       void* stream);
 
+/* ---- 8-bit products with a scale for each block of 128 --------------------
+   The products of a layer (projections, experts, LM head) on 8-bit operands:
+   codes in e4m3 (4 exponent, 3 mantissa bits, largest value 448; one byte
+   each) and fp32 scales.  The pages have no counterpart; half the bytes of
+   bf16 weights for a round that is bound by reading them.
+
+   Formats.  Activations [rows, K]: one scale for each row and block of 128
+   columns, stored by block: scale[kb * lds + r], kb = 0 .. ceil(K / 128) - 1.
+   Weights [N, K] (or `groups` such matrices, one after the other): one scale
+   for each 128 x 128 block, scale[(g * ceil(N / 128) + nb) * ceil(K / 128) + kb].
+   A value is code * scale.  Rows of codes start every `ld` bytes (a multiple
+   of 16, at least K) at a 16-byte aligned base; K need not be a multiple of
+   16: the bytes of a row behind column K are neither used nor written, but
+   up to the next multiple of 16 they are read.
+
+   All calls only enqueue work on `stream` (of the current device) and use no
+   workspace, so they may be captured into CUDA graphs and calls on different
+   streams do not disturb one another.  Zero rows are a valid call that does
+   nothing.  Outputs must not overlap inputs. */
+typedef enum dg_dtype { DG_BF16 = 0, DG_F16 = 1, DG_F32 = 2 } dg_dtype;
+typedef enum dg_act {
+  DG_ACT_NONE = 0,
+  DG_ACT_SWIGLU = 1,             /* silu(x[r, j]) * x[r, cols + j]: gate columns, then up columns */
+  DG_ACT_SWIGLU_INTERLEAVED = 2  /* silu(x[r, 2j]) * x[r, 2j + 1]: the expert layers' order */
+} dg_act;
+
+/* Quantise rows: d_x [x_rows, cols] (2 * cols with SwiGLU) of `dtype`, ldx
+   elements between rows -> codes d_q [rows, cols] and scales d_scale
+   [ceil(cols / 128)][lds].  Output row r takes row r of x, or with d_index
+   (device int32 [rows]) row d_index[r]; an index outside [0, x_rows) reads as
+   a row of zeros.  With a = max |x| of a block, raised to at least 2^-100:
+   scale = a / 448, code = e4m3(x * (448 / a)) (fp32; to nearest even, at most
+   +-448).  A block with a NaN or an infinity has scale NaN and codes 0.
+   SwiGLU is evaluated in fp32 with silu(z) = z / (1 + e^-z) and not rounded
+   before the quantisation. */
+dg_status dg_fp8_quantize(const void* d_x, int32_t dtype, int64_t ldx, int64_t x_rows, const int32_t* d_index,
+                          int32_t act, int64_t rows, int64_t cols, uint8_t* d_q, int64_t ldq, float* d_scale,
+                          int64_t lds, void* stream);
+/* Quantise weights: d_w [groups, rows, cols] of `dtype` (ldw elements between
+   rows, the groups one after the other) -> codes [groups, rows, cols] and one
+   scale per 128 x 128 block of each group, by the same rule. */
+dg_status dg_fp8_quantize_blocks(const void* d_w, int32_t dtype, int64_t ldw, int64_t groups, int64_t rows,
+                                 int64_t cols, uint8_t* d_q, int64_t ldq, float* d_scale, void* stream);
+
+/* out[m, n] = w[m] * sum_kb sa[kb, m] * sb[n / 128, kb] * sum_{k in block kb} A[m, k] B[n, k]
+   for activations A [M, K] (codes d_a, scales d_a_scale [ceil(K / 128)][lds])
+   and weights B [N, K]; w = d_row_weight (fp32 [M]) or 1 where it is NULL.
+   Sums in fp32; out [M, N] of out_dtype (dg_dtype), ldo elements between
+   rows, rounded once. */
+dg_status dg_fp8_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds, const uint8_t* d_b,
+                      int64_t ldb, const float* d_b_scale, int64_t M, int64_t N, int64_t K, const float* d_row_weight,
+                      void* d_out, int32_t out_dtype, int64_t ldo, void* stream);
+/* The same with the rows split among `groups` (1..1024) weight matrices B
+   [groups, N, K] (experts): rows [d_off[g], d_off[g + 1]) take matrix g.
+   d_off: device int32 [groups + 1], non-decreasing; groups may be empty.
+   Rows outside [d_off[0], d_off[groups]) are neither read nor written;
+   offsets outside [0, M] are held inside it. */
+dg_status dg_fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds,
+                              const uint8_t* d_b, int64_t ldb, const float* d_b_scale, const int32_t* d_off,
+                              int64_t groups, int64_t M, int64_t N, int64_t K, const float* d_row_weight, void* d_out,
+                              int32_t out_dtype, int64_t ldo, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,430 @@
+"""The 8-bit block-scaled operators on the GPU against plain 64-bit forms:
+quantisers bit for bit, products within bounds derived from their roundings
+(fp8_ref.product_bound), masks, strides, streams and graphs."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def _dg():
+    import discrete_diffusion_moe_b200 as dg
+    return dg
+
+
+def _hidden(rng, rows, K, dtype):
+    x = rng.standard_normal((rows, K)) * np.exp(rng.uniform(-3, 3, (rows, 1)))
+    return torch.from_numpy(x.astype(np.float32)).to(dtype)
+
+
+def _same_codes(q, want):
+    got = q.double().cpu().numpy()
+    assert got.shape == want.shape
+    bad = np.flatnonzero((got != want).ravel())
+    assert bad.size == 0, (bad[:5], got.ravel()[bad[:5]], want.ravel()[bad[:5]])
+
+
+def _same_scales(s, want):
+    got = s.cpu().numpy()
+    assert np.array_equal(got, want, equal_nan=True), np.flatnonzero((got != want).ravel())[:5]
+
+
+# ---- quantisers -------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 16), (3, 127), (2, 128), (5, 129), (1, 2816), (7, 2816), (33, 704),
+                                    (64, 1000), (129, 257)])
+def test_quantize_rows(rows, K, dtype):
+    dg = _dg()
+    x = _hidden(np.random.default_rng(rows * 7 + K), rows, K, dtype)
+    q, s = dg.fp8_quantize(x.cuda())
+    want_q, want_s = ref.quantize_rows(x.double().numpy())
+    _same_codes(q, want_q)
+    _same_scales(s, want_s)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_rows_special_values(dtype):
+    """Zero blocks, the smallest and largest values, a NaN and infinities."""
+    dg = _dg()
+    x = _hidden(np.random.default_rng(3), 9, 300, dtype)
+    fi = torch.finfo(dtype)
+    x[0] = 0.0
+    x[1, :128] = 0.0
+    x[2] = fi.smallest_normal
+    x[3] = fi.max
+    x[4, 5] = float("nan")
+    x[5, 130] = float("inf")
+    x[6, 299] = -float("inf")
+    x[7] = -0.0
+    x[8, 1:] = fi.tiny * fi.eps   # the smallest subnormal
+    q, s = dg.fp8_quantize(x.cuda())
+    want_q, want_s = ref.quantize_rows(x.double().numpy())
+    _same_codes(q, want_q)
+    _same_scales(s, want_s)
+    assert np.isnan(want_s).sum() == 3
+
+
+@pytest.mark.parametrize("K", [704, 130, 99])
+def test_quantize_gathered_rows(K):
+    """Rows taken by index, the same index twice; indices outside x give zeros."""
+    dg = _dg()
+    rng = np.random.default_rng(K)
+    x = _hidden(rng, 40, K, torch.bfloat16)
+    index = torch.from_numpy(rng.integers(0, 40, 77).astype(np.int32))
+    index[3], index[9], index[20] = -1, 40, 2 ** 31 - 1
+    q, s = dg.fp8_quantize(x.cuda(), index=index.cuda())
+    src = torch.zeros(77, K, dtype=torch.bfloat16)
+    inside = (index >= 0) & (index < 40)
+    src[inside] = x[index[inside].long()]
+    want_q, want_s = ref.quantize_rows(src.double().numpy())
+    _same_codes(q, want_q)
+    _same_scales(s, want_s)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["swiglu", "swiglu_interleaved"])
+@pytest.mark.parametrize("rows,K", [(1, 704), (9, 704), (33, 129), (4, 1), (17, 1000)])
+def test_quantize_swiglu(rows, K, act, dtype):
+    dg = _dg()
+    rng = np.random.default_rng(rows + K)
+    y = torch.from_numpy((4 * rng.standard_normal((rows, 2 * K))).astype(np.float32)).to(dtype)
+    y[0, :] *= 10.0   # gates far into silu's limits
+    q, s = dg.fp8_quantize(y.cuda(), act=act)
+    d = y.double().numpy()
+    g, u = (d[:, :K], d[:, K:]) if act == "swiglu" else (d[:, 0::2], d[:, 1::2])
+    v = ref.swiglu(g, u)
+    # e^-g: 2 units plus the rounding of g log2(e) (|g| 2^-24 of e^-g each way),
+    # the sum, the quotient (2 units) and the product with u: (7 + 2 |g|) 2^-24
+    # for positive g; for negative g the denominator is e^-g itself: the same
+    rel = (8 + 2 * np.abs(g)) * 2.0 ** -23
+    got_s = s.double().cpu().numpy()
+    for kb in range(ref.blocks(K)):
+        sl = slice(kb * 128, min(K, kb * 128 + 128))
+        amax = np.maximum(np.abs(v[:, sl]).max(1), ref.AMAX_MIN)
+        assert np.all(np.abs(got_s[kb] - amax / 448) <= (rel[:, sl].max(1) + 2.0 ** -23) * amax / 448)
+    got = ref.dequantize_rows(q, s)
+    step = np.repeat(got_s.T, 128, axis=1)[:, :K]
+    # half a step of a normal code is 2^-4 of the value, of a subnormal one 2^-10;
+    # the largest values may be held to 448: off by the scale's own error
+    bound = (2.0 ** -4 + 2 * rel + 2.0 ** -20) * np.abs(v) + 2.0 ** -10 * step
+    assert np.all(np.abs(got - v) <= bound), float((np.abs(got - v) / bound).max())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("G,N,K", [(None, 1, 1), (None, 128, 128), (None, 130, 257), (2, 64, 704), (3, 129, 99), (1, 300, 1024)])
+def test_quantize_blocks(G, N, K, dtype):
+    dg = _dg()
+    rng = np.random.default_rng(N + K)
+    shape = (N, K) if G is None else (G, N, K)
+    w = torch.from_numpy((rng.standard_normal(shape) * 0.02).astype(np.float32)).to(dtype)
+    if N > 128:
+        w[..., 0, 0] = float("nan")
+        w[..., 128:, :128] = 0.0
+    q, s = dg.fp8_quantize_blocks(w.cuda())
+    d = w.double().numpy().reshape(-1, N, K)
+    for g in range(d.shape[0]):
+        want_q, want_s = ref.quantize_blocks(d[g])
+        _same_codes(q.reshape(-1, N, K)[g] if G is None else q[g], want_q)
+        _same_scales(s if G is None else s[g], want_s)
+
+
+def test_quantize_strides_and_given_outputs():
+    """Views of wider tensors in and out: what lies between the rows stays."""
+    dg = _dg()
+    rng = np.random.default_rng(11)
+    wide = _hidden(rng, 20, 400, torch.bfloat16).cuda()
+    for x in (wide[:, :256], wide[:, 3:260], wide[::2, 8:264]):
+        rows, K = x.shape
+        buf = torch.full((rows, 400), 0x55, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        sbuf = torch.full((ref.blocks(K) + 1, rows + 5), -1.0, device="cuda")
+        out = (buf[:, :K], sbuf[:ref.blocks(K), :rows])
+        q, s = dg.fp8_quantize(x, out=out)
+        assert q.data_ptr() == buf.data_ptr()
+        want_q, want_s = ref.quantize_rows(x.double().cpu().numpy())
+        _same_codes(q, want_q)
+        _same_scales(s, want_s)
+        assert torch.all(buf.view(torch.uint8)[:, K:] == 0x55)
+        assert torch.all(sbuf[:, rows:] == -1.0) and torch.all(sbuf[-1] == -1.0)
+
+
+# ---- products ----------------------------------------------------------------------
+
+def _check(got, want, want_abs, K, weighted=False):
+    out = got.double().cpu().numpy()
+    bound = ref.product_bound(want, want_abs, K, got.dtype, weighted)
+    err = np.abs(out - want)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("out_dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 16, 16), (3, 5, 7), (1, 5632, 2816), (8, 704, 2816), (9, 130, 385), (16, 1408, 128), (17, 256, 2816),
+    (64, 33, 1000), (127, 257, 129), (128, 128, 128), (129, 640, 704), (256, 2816, 2816), (255, 1001, 1111),
+    (300, 384, 8192), (1000, 513, 256), (2, 20000, 64), (513, 96, 90)])
+def test_gemm(M, N, K, out_dtype):
+    dg = _dg()
+    rng = np.random.default_rng(M + N + K)
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K)
+    got = dg.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype)
+    if out_dtype == torch.float16:   # the whole e4m3 range overflows fp16: smaller scales
+        sa = sa * 2.0 ** -14
+        got = dg.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype)
+    want, want_abs = ref.product(ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb))
+    _check(got, want, want_abs, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 100, 300), (5, 100, 300), (40, 100, 300), (300, 300, 300)])
+def test_gemm_strides_weights_and_given_output(M, N, K):
+    """Wider pitches (with NaN codes between the rows), row weights, and an
+    output whose rows are views: nothing beside them is written."""
+    dg = _dg()
+    rng = np.random.default_rng(M)
+    a, sa = ref.random_operand(rng, M, K, pitch=368)
+    b, sb = ref.random_weights(rng, N, K, pitch=512)
+    sa_wide = torch.full((sa.shape[0], M + 3), float("nan"), device="cuda")
+    sa_wide[:, 1:M + 1] = sa
+    sa = sa_wide[:, 1:M + 1]
+    w = torch.from_numpy(rng.standard_normal(M).astype(np.float32)).cuda()
+    for dtype, ld, first in ((torch.bfloat16, N + 12, 0), (torch.bfloat16, N + 7, 3), (torch.float32, N + 5, 1)):
+        buf = torch.full((M + 1, ld), -7.0, dtype=dtype, device="cuda")
+        out = buf[:M, first:first + N]
+        got = dg.fp8_gemm(a, sa, b, sb, row_weight=w, out=out)
+        assert got.data_ptr() == out.data_ptr()
+        want, want_abs = ref.product(ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb))
+        wd = w.double().cpu().numpy()[:, None]
+        _check(got, want * wd, want_abs * np.abs(wd), K, weighted=True)
+        rest = torch.ones_like(buf, dtype=torch.bool)
+        rest[:M, first:first + N] = False
+        assert torch.all(buf[rest] == -7.0)
+
+
+@pytest.mark.parametrize("M", [1, 12, 200])
+def test_gemm_nan_stays_in_its_row_and_column(M):
+    """A NaN scale makes exactly its row's (its 128 columns') results NaN; so
+    does a NaN code for its row."""
+    dg = _dg()
+    N, K = 300, 400
+    rng = np.random.default_rng(M)
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K)
+    sa[1, M // 2] = float("nan")
+    sb[1, 3] = float("nan")
+    a.view(torch.uint8)[M - 1, 17] = 0x7F
+    got = torch.isnan(dg.fp8_gemm(a, sa, b, sb))
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[M // 2] = want[M - 1] = True
+    want[:, 128:256] = True
+    assert torch.equal(got.cpu(), want)
+
+
+def _sizes(rng, G, rows, empty):
+    w = rng.random(G) ** 3
+    w[rng.permutation(G)[:empty]] = 0
+    return rng.multinomial(rows, w / w.sum())
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1], 16, 16), ([0, 1, 0], 40, 100), ([1] * 8, 704, 256), ([3, 0, 0, 17, 1], 130, 704), ([0, 0, 300], 257, 129),
+    ([128, 256, 129, 0, 255], 384, 384), ([5] * 40, 96, 128), ([1000, 1], 200, 64), ([0, 64, 0, 0, 700, 2], 1408, 300)])
+def test_grouped_gemm(sizes, N, K, out_dtype):
+    """Ragged groups, empty ones, rows before the first and behind the last."""
+    dg = _dg()
+    G, lead, tail = len(sizes), 2, 3
+    rng = np.random.default_rng(sum(sizes) + N + K)
+    M = lead + sum(sizes) + tail
+    off = np.concatenate([[0], np.cumsum(sizes)]) + lead
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K, G=G)
+    w = torch.from_numpy(rng.random(M).astype(np.float32)).cuda()
+    out = torch.full((M, N), -3.0, dtype=out_dtype, device="cuda")
+    got = dg.fp8_grouped_gemm(a, sa, b, sb, torch.from_numpy(off.astype(np.int32)).cuda(), row_weight=w, out=out)
+    av, bv, wd = ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb), w.double().cpu().numpy()[:, None]
+    for g in range(G):
+        r = slice(off[g], off[g + 1])
+        want, want_abs = ref.product(av[r], bv[g])
+        _check(got[r], want * wd[r], want_abs * wd[r], K, weighted=True)
+    assert torch.all(out[:lead] == -3.0) and torch.all(out[M - tail:] == -3.0)
+
+
+@pytest.mark.parametrize("G,rows,empty", [(16, 512, 4), (128, 2048, 44), (128, 200, 60), (1000, 1500, 500)])
+def test_grouped_gemm_like_an_expert_layer(G, rows, empty):
+    dg = _dg()
+    N, K = 160, 192
+    rng = np.random.default_rng(G + rows)
+    sizes = _sizes(rng, G, rows, empty)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    a, sa = ref.random_operand(rng, rows, K)
+    b, sb = ref.random_weights(rng, N, K, G=G)
+    got = dg.fp8_grouped_gemm(a, sa, b, sb, torch.from_numpy(off.astype(np.int32)).cuda())
+    av, bv = ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb)
+    for g in range(G):
+        r = slice(off[g], off[g + 1])
+        _check(got[r], *ref.product(av[r], bv[g]), K)
+
+
+def test_grouped_gemm_offsets_outside_are_held_inside():
+    dg = _dg()
+    N, K, M = 48, 80, 30
+    rng = np.random.default_rng(5)
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K, G=3)
+    out = torch.full((M, N), -3.0, device="cuda")
+    dg.fp8_grouped_gemm(a, sa, b, sb, torch.tensor([-9, 4, 20, 1000], dtype=torch.int32, device="cuda"), out=out)
+    av, bv = ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb)
+    for g, (lo, hi) in enumerate([(0, 4), (4, 20), (20, 30)]):
+        _check(out[lo:hi], *ref.product(av[lo:hi], bv[g]), K)
+
+
+def test_no_rows():
+    dg = _dg()
+    rng = np.random.default_rng(1)
+    b, sb = ref.random_weights(rng, 32, 64, G=2)
+    a = torch.empty(0, 64, dtype=torch.float8_e4m3fn, device="cuda")
+    sa = torch.empty(1, 0, device="cuda")
+    assert dg.fp8_gemm(a, sa, b[0], sb[0]).shape == (0, 32)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert dg.fp8_grouped_gemm(a, sa, b, sb, off).shape == (0, 32)
+    q, s = dg.fp8_quantize(torch.empty(0, 64, device="cuda"))
+    assert q.shape == (0, 64) and s.shape == (1, 0)
+    # groups that are all empty: nothing is written
+    a, sa = ref.random_operand(rng, 5, 64)
+    out = torch.full((5, 32), 2.0, device="cuda")
+    dg.fp8_grouped_gemm(a, sa, b, sb, off, out=out)
+    assert torch.all(out == 2.0)
+
+
+# ---- as they are used together ----------------------------------------------------------
+
+def _expert_block(dg, x, index, off, w1, w2, row_weight):
+    """Gather + quantise, gate/up, SwiGLU + quantise, down with routing weights."""
+    q, s = dg.fp8_quantize(x, index=index)
+    y = dg.fp8_grouped_gemm(q, s, *w1, off)
+    h, hs = dg.fp8_quantize(y, act="swiglu_interleaved")
+    return (q, s), y, (h, hs), dg.fp8_grouped_gemm(h, hs, *w2, off, row_weight=row_weight, out_dtype=torch.float32)
+
+
+def _expert_inputs(T, k, G, d, f, seed=0):
+    dg = _dg()
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).to(torch.bfloat16).cuda()
+    expert = np.stack([rng.permutation(G)[:k] for _ in range(T)]).ravel()
+    order = np.argsort(expert, kind="stable")
+    off = np.concatenate([[0], np.cumsum(np.bincount(expert, minlength=G))]).astype(np.int32)
+    w1 = dg.fp8_quantize_blocks(torch.from_numpy((rng.standard_normal((G, 2 * f, d)) * 0.05).astype(np.float32)).cuda())
+    w2 = dg.fp8_quantize_blocks(torch.from_numpy((rng.standard_normal((G, d, f)) * 0.05).astype(np.float32)).cuda())
+    index = torch.from_numpy((order // k).astype(np.int32)).cuda()
+    rw = torch.from_numpy(rng.random(T * k).astype(np.float32)).cuda()
+    return x, index, torch.from_numpy(off).cuda(), w1, w2, rw
+
+
+@pytest.mark.parametrize("T,k,G,d,f", [(1, 2, 16, 256, 512), (1, 8, 32, 320, 192), (64, 2, 16, 256, 512), (256, 4, 8, 256, 96)])
+def test_expert_block_stage_by_stage(T, k, G, d, f):
+    """Each stage against the 64-bit form on the stage's own input."""
+    dg = _dg()
+    x, index, off, w1, w2, rw = _expert_inputs(T, k, G, d, f)
+    (q, s), y, (h, hs), out = _expert_block(dg, x, index, off, w1, w2, rw)
+    want_q, want_s = ref.quantize_rows(x.double().cpu().numpy()[index.cpu().numpy()])
+    _same_codes(q, want_q)
+    _same_scales(s, want_s)
+    o = off.cpu().numpy()
+    qv, hv = ref.dequantize_rows(q, s), ref.dequantize_rows(h, hs)
+    w1v, w2v = ref.dequantize_blocks(*w1), ref.dequantize_blocks(*w2)
+    wd = rw.double().cpu().numpy()[:, None]
+    for g in range(G):
+        r = slice(o[g], o[g + 1])
+        _check(y[r], *ref.product(qv[r], w1v[g]), d)
+        want, want_abs = ref.product(hv[r], w2v[g])
+        _check(out[r], want * wd[r], want_abs * wd[r], f, weighted=True)
+    yd = y.double().cpu().numpy()
+    v = ref.swiglu(yd[:, 0::2], yd[:, 1::2])
+    step = np.repeat(hs.double().cpu().numpy().T, 128, axis=1)[:, :f]
+    assert np.all(np.abs(hv - v) <= (2.0 ** -4 + 2.0 ** -15) * np.abs(v) + 2.0 ** -10 * step)
+
+
+def test_streams_and_captured_graphs_give_the_same_bits():
+    """The block on the current stream, on two streams at once, and replayed
+    from two graphs that run at the same time on new inputs."""
+    dg = _dg()
+    a_in, b_in = _expert_inputs(96, 4, 16, 256, 192, seed=1), _expert_inputs(40, 4, 16, 256, 192, seed=2)
+    want = [_expert_block(dg, *i)[-1].clone() for i in (a_in, b_in)]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [None, None]
+    for _ in range(3):
+        for n, (st, i) in enumerate(((s1, a_in), (s2, b_in))):
+            with torch.cuda.stream(st):
+                got[n] = _expert_block(dg, *i)[-1]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    graphs, outs = [], []
+    xs = [a_in[0].clone(), b_in[0].clone()]
+    for st, i, x in ((s1, a_in, xs[0]), (s2, b_in, xs[1])):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            outs.append(_expert_block(dg, x, *i[1:])[-1])
+        graphs.append(g)
+    for x in xs:
+        x.mul_(-1.5)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, g in zip((s1, s2), graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for n, (i, x) in enumerate(((a_in, xs[0]), (b_in, xs[1]))):
+        assert torch.equal(outs[n], _expert_block(dg, x, *i[1:])[-1])
+
+
+def test_given_stream():
+    dg = _dg()
+    rng = np.random.default_rng(8)
+    a, sa = ref.random_operand(rng, 33, 256)
+    b, sb = ref.random_weights(rng, 70, 256)
+    want = dg.fp8_gemm(a, sa, b, sb)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = dg.fp8_gemm(a, sa, b, sb, stream=st)
+    q, s = dg.fp8_quantize(want, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+    assert torch.equal(q.view(torch.uint8), dg.fp8_quantize(want)[0].view(torch.uint8))
+
+
+def test_python_refusals():
+    """Wrong shapes, types and strides are refused before any launch."""
+    dg = _dg()
+    rng = np.random.default_rng(9)
+    a, sa = ref.random_operand(rng, 8, 64)
+    b, sb = ref.random_weights(rng, 32, 64)
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = torch.zeros(4, 64, device="cuda")
+    for call in (
+            lambda: dg.fp8_gemm(a.float(), sa, b, sb), lambda: dg.fp8_gemm(a, sa[:, :7], b, sb),
+            lambda: dg.fp8_gemm(a, sa.double(), b, sb), lambda: dg.fp8_gemm(a[:, :32], sa, b, sb),
+            lambda: dg.fp8_gemm(a, sa, b, sb.expand(2, 1)), lambda: dg.fp8_gemm(a, sa, b, sb, out_dtype=torch.float64),
+            lambda: dg.fp8_gemm(a, sa, b, sb, out=torch.empty(8, 31, device="cuda")),
+            lambda: dg.fp8_gemm(a, sa, b, sb, out=torch.empty(32, 8, device="cuda").t()),
+            lambda: dg.fp8_gemm(a, sa, b, sb, row_weight=torch.ones(7, device="cuda")),
+            lambda: dg.fp8_gemm(a, sa.cpu(), b, sb), lambda: dg.fp8_gemm(a[:, ::2], sa, b[:, ::2], sb),
+            lambda: dg.fp8_grouped_gemm(a, sa, b, sb, off), lambda: dg.fp8_grouped_gemm(a, sa, b[None], sb[None], None),
+            lambda: dg.fp8_grouped_gemm(a, sa, b[None], sb[None], off.long()),
+            lambda: dg.fp8_grouped_gemm(a, sa, b[None], sb[None], off[:1]),
+            lambda: dg.fp8_quantize(x.double()), lambda: dg.fp8_quantize(x, act="relu"), lambda: dg.fp8_quantize(x.t()),
+            lambda: dg.fp8_quantize(x[:, :63], act="swiglu"), lambda: dg.fp8_quantize(x, index=off.long()),
+            lambda: dg.fp8_quantize(x, out=(a, sa)), lambda: dg.fp8_quantize_blocks(x[0]),
+            lambda: dg.fp8_quantize_blocks(x.t()), lambda: dg.fp8_quantize_blocks(x.view(2, 2, 64).transpose(0, 1))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(dg.DgError):   # rows of 40 bytes cannot start on 16-byte boundaries
+        odd = torch.zeros(8, 40, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        dg.fp8_gemm(odd, sa, torch.zeros(32, 48, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)[:, :40], sb)
