@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "../../include/dg.h"
+#include "fp8_gemm.cuh"
 #include "fp8_quant.cuh"
 #include "fp8_small.cuh"
 #include "host.cuh"
@@ -14,7 +15,6 @@ using namespace dg;
 namespace {
 
 constexpr long long kMaxDim = 2147483647ll;
-constexpr int kFp8MaxGroups = 1024;
 
 size_t dtype_bytes(int dt) { return dt == DG_F32 ? 4 : 2; }
 bool dtype_ok(int dt) { return dt == DG_BF16 || dt == DG_F16 || dt == DG_F32; }
@@ -56,11 +56,54 @@ dg_status launch_small(const Fp8GemmParams& p, cudaStream_t st) {
   return DG_OK;
 }
 
+// Codes [rows, K] with `pitch` bytes between rows as a tensor of bytes; boxes of
+// 128 columns (one block) x box_rows with the 128-byte swizzle.  Columns and
+// rows outside read as zero codes.
+dg_status make_tmap_codes(CUtensorMap* m, const uint8_t* base, long long K, long long rows, long long pitch,
+                          int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)pitch};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return DG_OK;
+}
+
+template <int kBN, class TO>
+dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
+  using S = Fp8Shape<kBN>;
+  Fp8Maps maps;
+  const int a_rows[3] = {16, 64, 128};
+  for (int i = 0; i < 3; ++i) DG_TRY(make_tmap_codes(&maps.a[i], p.a, p.K, p.M, p.lda, a_rows[i]));
+  for (int i = 0; i < 2; ++i) DG_TRY(make_tmap_codes(&maps.b[i], p.b, p.K, (long long)p.G * p.N, p.ldb, kBN / (i ? 2 : 4)));
+  const void* fn = (const void*)fp8_pair_kernel<kBN, TO>;
+  DG_TRY(set_smem_attr(fn, S::kSmem, true));
+  const long long tiles = p.off ? std::min(p.G, p.M) + (long long)p.M / 256 : ceil_div(p.M, 256);  // at most
+  const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, tiles * ceil_div(p.N, kBN));
+  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kBN, TO>, maps, p));
+  return DG_OK;
+}
+
+template <class TO>
+dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
+  if (p.M <= 16) return launch_small<TO>(p, st);
+  const int pairs = device_sms() / 2;
+  const long long tiles = p.off ? std::max<long long>(std::min(p.G, p.M), p.M / 256) : ceil_div(p.M, 256);
+  if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<256, TO>(p, pairs, st);
+  if (tiles * ceil_div(p.N, 128) >= pairs / 2) return launch_pair<128, TO>(p, pairs, st);
+  return launch_pair<64, TO>(p, pairs, st);
+}
+
 dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, cudaStream_t st) {
   switch (out_dtype) {
-    case DG_BF16: return launch_small<__nv_bfloat16>(p, st);
-    case DG_F16: return launch_small<__half>(p, st);
-    case DG_F32: return launch_small<float>(p, st);
+    case DG_BF16: return launch_product<__nv_bfloat16>(p, st);
+    case DG_F16: return launch_product<__half>(p, st);
+    case DG_F32: return launch_product<float>(p, st);
     default: return fail(DG_ERR_INVALID_ARG, "%s: output type %d", who, out_dtype);
   }
 }
