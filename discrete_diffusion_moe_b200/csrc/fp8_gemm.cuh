@@ -9,26 +9,32 @@
 // accumulator element.  (With the weights as rows every column would need its
 // own scale from shared memory.)
 //
-// A unit is 256 rows x kBN columns of one group.  Per block of 128 k (one
-// stage: 128 bytes of each row, the width of the 128-byte swizzle) the
-// leader issues four tcgen05.mma of M = 256, K = 32 into a fresh tensor-memory
-// buffer; eight epilogue warps in each CTA take the block's sums out, multiply
-// them by the scales and add them in registers, while the tensor cores work on
-// the next block in another buffer.  fp32 throughout; one rounding at the
-// store.  The fixed scale per 128 is why the sums leave tensor memory at every
-// block: a 128 x 256 block takes the tensor cores 512 cycles, and its 256
-// tcgen05.ld'ed columns per lane quarter are shared by two warps.
+// A unit is 256 rows x (kW * kH) columns of one group.  Per block of 128 k (one
+// stage: 128 bytes of each row, the width of the 128-byte swizzle) the leader
+// issues, for each of the kH column parts, four tcgen05.mma of M = 256, N = kW,
+// K = 32 into a fresh tensor-memory buffer; eight epilogue warps in each CTA
+// take the part's sums out, multiply them by the scales and add them in
+// registers, while the tensor cores work on the next parts in the other three
+// buffers.  fp32 throughout; one rounding at the store.  Parts of 128 columns
+// and four buffers, not 256 and two: a buffer goes around through the commit,
+// the epilogue and the release to the other CTA's leader, about 1000 cycles
+// beside its MMAs, which two buffers cannot hide.
 //
 // Each CTA of a pair copies its own 128 rows of A and half of the columns of B
-// (32 KB a stage at kBN = 256), so a pair reads (256 + kBN) rows per block.
-// Copies of few rows use a smaller box (16 or 64 rows): the rest of the tile
-// holds old bytes, and only rows that are not stored depend on them.
+// (32 KB a stage at 256 columns), so a pair reads 512 rows per block.  Copies of
+// few rows use a smaller box (16 or 64 rows): the rest of the tile holds old
+// bytes, and only rows that are not stored depend on them.
+//
+// The results are turned through shared memory so that a warp stores whole
+// 128-byte lines (a thread holds one row; storing from registers touched 32
+// lines per instruction and took a sixth of a unit's time).
 //
 // Protocol of the barriers (rank 0 leads):
-//   full[s]       rank 0's: both CTAs' copies of a stage have landed
-//   empty[s]      both: the MMAs that read the stage are done
-//   acc_full[b]   both: the block's sums are in tensor memory
-//   acc_empty[b]  rank 0's: all 16 epilogue warps have read them
+//   full[s]         rank 0's: both CTAs' copies of a stage have landed
+//   acc_full[h][s]  both: part h's sums of the stage's block are in tensor
+//                   memory; the last part's also frees the stage
+//   acc_empty[b]    rank 0's: all 16 epilogue warps have read the buffer
+//   sc_full, sc_empty[i]  each CTA's own: a slot of scales is written, is read
 // All waits are bounded; after one runs out the CTA stops working and stores
 // NaN for what it could not compute.
 #pragma once
@@ -42,8 +48,27 @@ namespace dg {
 
 constexpr int kFp8MaxGroups = 1024;
 constexpr int kFp8EpiWarps = 8;
-constexpr int kFp8Threads = 64 + 32 * kFp8EpiWarps;
+// Warpgroup 0: the copying warp, the MMA warp and two idle ones; warpgroups 1 and 2:
+// the epilogue.  384 threads x 168 registers at launch; warpgroup 0 gives back what
+// the epilogue takes.  Nothing may spill: with nearly all of the SM's memory used
+// as shared memory a spilled register comes back from L2 (measured: 400 cycles a
+// part, half of the kernel's time).
+constexpr int kFp8Threads = 128 + 32 * kFp8EpiWarps;
+constexpr int kFp8RegsCopy = 72, kFp8RegsEpi = 216;
+static_assert(128 * kFp8RegsCopy + 32 * kFp8EpiWarps * kFp8RegsEpi <= kFp8Threads * 168, "register split");
 
+// One lane of a converged warp.  The copies and MMAs take their descriptors from
+// uniform registers; issued from a branch on the lane number the compiler moves
+// them there one instruction at a time, which measured 120 cycles each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // instruction descriptor of tcgen05.mma kind::f8f6f4: D fp32, A and B e4m3, both K-major
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -56,6 +81,48 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, 
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// Bounded wait without a result: when it runs out, *dead is set (then later waits
+// end at once) and the caller goes on; the kernel's results are marked at their
+// store.  Warps are converged again after it.
+__device__ __forceinline__ void wait_or_die(uint32_t bar, uint32_t parity, volatile int* dead) {
+  if (!mbar_try_wait(bar, parity)) {
+    const unsigned long long t0 = globaltimer_ns();
+    uint32_t n = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+      if ((++n & 255u) == 0u && (*dead || globaltimer_ns() - t0 > kWaitLimitNs)) {
+        *dead = 1;
+        break;
+      }
+    }
+  }
+  __syncwarp();
+}
+// 32 lanes x 32 consecutive fp32 columns of tensor memory; the registers are
+// undefined until tmem_wait32 on them
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
 }
 // Arrive on a pair peer's (or this CTA's) mbarrier at the default scope.  What it
 // orders are tensor-memory reads, by the tcgen05 fence before it; a release at
@@ -75,7 +142,7 @@ __device__ __forceinline__ uint64_t pack2(float v) {
   return ((uint64_t)u << 32) | u;
 }
 
-// tensor maps: A with boxes of 16, 64 and 128 rows, B with boxes of kBN / 4 and kBN / 2 rows
+// tensor maps: A with boxes of 16, 64 and 128 rows, B with boxes of kW / 4 and kW / 2 rows
 struct Fp8Maps {
   CUtensorMap a[3];
   CUtensorMap b[2];
@@ -118,70 +185,111 @@ __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Table
   return j;
 }
 
-template <int kBN>
+template <int kW, int kH>
 struct Fp8Shape {
-  static constexpr int kStageA = 128 * 128, kStageB = (kBN / 2) * 128, kStage = kStageA + kStageB;
-  static constexpr int kBufs = kBN >= 256 ? 2 : 4;  // tensor-memory buffers of kBN columns
-  static constexpr int kStages = kBN >= 256 ? 6 : 8;
-  static constexpr int kSmem = 1024 + kStages * kStage + (2 * kStages + 2 * kBufs + 1) * 8 + 16;
+  static constexpr int kBN = kW * kH;
+  static constexpr int kBufs = 4;  // tensor-memory buffers of kW columns
+  static constexpr int kStages = kBN >= 256 ? 5 : (kBN >= 128 ? 6 : 8);
+  static constexpr int kStageA = 128 * 128, kPartB = (kW / 2) * 128, kStage = kStageA + kH * kPartB;
+  static constexpr int kTurn = kFp8EpiWarps * 4096;  // 32 rows x 128 bytes per warp
+  // row and weight scales of four blocks per slot: [4][128] and [4][kH] floats
+  static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * kH;
+  static constexpr int kBars = kStages * (1 + kH) + kBufs + 2 * kScaleSlots + 1;
+  static constexpr int kSmem = 1024 + kStages * kStage + kTurn + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
 };
 
-// eight results of one row from column 0 of `o` on, `n` of them valid
-template <class TO>
-__device__ __forceinline__ void store8(TO* o, const float (&v)[8], int n, bool vec) {
-  if (vec && n >= 8) {
-    if constexpr (sizeof(TO) == 4) {
-      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t w[4];
+// Stores a warp's 32 rows x kCols results (thread `lane` holds row lane in v)
+// through its 4 KB of shared memory, 128 bytes of each row at a time, 16-byte
+// units swizzled by row: both sides are free of bank conflicts.  Rows from
+// `rows` on and columns from `cols` on are not stored.
+template <class TO, int kCols>
+__device__ __forceinline__ void store_turned(uint8_t* turn, TO* out, long long ldo, const uint64_t* acc, float w,
+                                             int lane, int rows, int cols, bool vec) {
+  constexpr int kPer = 128 / (int)sizeof(TO);       // columns per pass
+  constexpr int kPass = kCols < kPer ? kCols : kPer;
+  constexpr int kUnit = 16 / (int)sizeof(TO);       // columns per 16-byte unit
+  constexpr int kUnits = kPass / kUnit;
+#pragma unroll
+  for (int c0 = 0; c0 < kCols; c0 += kPass) {
+    if (c0 >= cols) break;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      uint32_t x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (std::is_same_v<TO, __half>) w[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
-        else w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        if constexpr (sizeof(TO) == 4) {
+          const uint64_t a = acc[(c0 + u * kUnit + i) >> 1];
+          x[i] = __float_as_uint(__uint_as_float((uint32_t)((i & 1) ? (a >> 32) : a)) * w);
+        } else {
+          const uint64_t a = acc[(c0 + u * kUnit + 2 * i) >> 1];
+          const float lo = __uint_as_float((uint32_t)a) * w, hi = __uint_as_float((uint32_t)(a >> 32)) * w;
+          if constexpr (std::is_same_v<TO, __half>) x[i] = pack_f16x2(lo, hi);
+          else x[i] = pack_bf16x2(lo, hi);
+        }
       }
-      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(turn + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
     }
-  } else {
+    __syncwarp();
+    if (vec && c0 + kPass <= cols) {
+      constexpr int kRowsPer = 32 / kUnits;  // rows per store instruction
+      const int u = lane % kUnits;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) store_out(o + i, v[i]);
+      for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
+        const int r = r0 + lane / kUnits;
+        const uint4 q = *reinterpret_cast<const uint4*>(turn + r * 128 + ((u ^ (r & 7)) * 16));
+        if (r < rows) *reinterpret_cast<uint4*>(out + r * ldo + c0 + u * kUnit) = q;
+      }
+    } else {
+      const int n = min(kPass, cols - c0);
+      for (int r = 0; r < rows; ++r)
+        for (int c = lane; c < n; c += 32)
+          out[r * ldo + c0 + c] =
+              *reinterpret_cast<const TO*>(turn + r * 128 + (((c / kUnit) ^ (r & 7)) * 16) + (c % kUnit) * sizeof(TO));
+    }
+    __syncwarp();
   }
 }
 
-template <int kBN, class TO>
+template <int kW, int kH, class TO>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8GemmParams p) {
-  using S = Fp8Shape<kBN>;
-  constexpr int kHalf = kBN / 2;             // columns of an epilogue warp
-  constexpr int kAhead = kBN >= 256 ? 2 : 4;  // blocks of scales loaded ahead
+  using S = Fp8Shape<kW, kH>;
+  constexpr int kHalf = kW / 2;  // columns of each part that an epilogue warp takes
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Fp8Tables tabs;
+  __shared__ int s_dead;
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const sA = smem;
-  uint8_t* const sB = smem + S::kStages * S::kStageA;
-  uint64_t* const full = (uint64_t*)(sB + S::kStages * S::kStageB);
-  uint64_t* const empty = full + S::kStages;
-  uint64_t* const acc_full = empty + S::kStages;
-  uint64_t* const acc_empty = acc_full + S::kBufs;
-  uint64_t* const drain = acc_empty + S::kBufs;
-  uint32_t* const tmem_slot = (uint32_t*)(drain + 1);
+  uint8_t* const sB = sA + S::kStages * S::kStageA;
+  uint8_t* const s_turn = sB + S::kStages * kH * S::kPartB;
+  float* const s_scale = (float*)(s_turn + S::kTurn);
+  uint64_t* const bars = (uint64_t*)(s_scale + S::kScaleSlots * S::kScaleSlot);
+  uint32_t* const tmem_slot = (uint32_t*)(bars + S::kBars);
+  const uint32_t full = smem_u32(bars);
+  const uint32_t acc_full = full + 8 * S::kStages;            // [kH][kStages]
+  const uint32_t acc_empty = acc_full + 8 * kH * S::kStages;  // [kBufs]
+  const uint32_t sc_full = acc_empty + 8 * S::kBufs;          // [kScaleSlots]
+  const uint32_t sc_empty = sc_full + 8 * S::kScaleSlots;
+  const uint32_t drain = sc_empty + 8 * S::kScaleSlots;
+  volatile int* const dead = &s_dead;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
-  const int n_tiles = (p.N + kBN - 1) / kBN;
+  const int n_tiles = (p.N + S::kBN - 1) / S::kBN;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(full + 8 * s, 1);
+      for (int h = 0; h < kH; ++h) mbar_init(acc_full + 8 * (h * S::kStages + s), 1);
     }
-    for (int b = 0; b < S::kBufs; ++b) {
-      mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 2 * kFp8EpiWarps);
+    for (int b = 0; b < S::kBufs; ++b) mbar_init(acc_empty + 8 * b, 2 * kFp8EpiWarps);
+    for (int i = 0; i < S::kScaleSlots; ++i) {
+      mbar_init(sc_full + 8 * i, 32);
+      mbar_init(sc_empty + 8 * i, kFp8EpiWarps);
     }
-    mbar_init(smem_u32(drain), 1);
+    mbar_init(drain, 1);
+    s_dead = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
     for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.a[i]);
@@ -190,34 +298,32 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   grid_dep_wait();
   grid_dep_launch();
   int m_tiles = (p.M + 255) / 256;
-  if (p.off) {
-    if (warp == 2) {
-      int sum = 0;
-      for (int base = 0; base < p.G; base += 32) {
-        const int g = base + lane;
-        RowRange r{0, 0};
-        if (g < p.G) r = group_rows(p.off, g, p.M);
-        const int t = (r.row1 - r.row0 + 255) / 256;
-        int inc = t;
+  if (p.off && warp == 4) {
+    int sum = 0;
+    for (int base = 0; base < p.G; base += 32) {
+      const int g = base + lane;
+      RowRange r{0, 0};
+      if (g < p.G) r = group_rows(p.off, g, p.M);
+      const int t = (r.row1 - r.row0 + 255) / 256;
+      int inc = t;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        if (g < p.G) {
-          tabs.first[g] = sum + inc - t;
-          tabs.row0[g] = r.row0;
-          tabs.row1[g] = r.row1;
-        }
-        sum += __shfl_sync(0xffffffffu, inc, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
       }
-      if (lane == 0) tabs.first[p.G] = sum;
+      if (g < p.G) {
+        tabs.first[g] = sum + inc - t;
+        tabs.row0[g] = r.row0;
+        tabs.row1[g] = r.row1;
+      }
+      sum += __shfl_sync(0xffffffffu, inc, 31);
     }
+    if (lane == 0) tabs.first[p.G] = sum;
   }
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers initialised before either signals one
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), S::kBufs * kBN);
+    tmem_alloc_pair(smem_u32(tmem_slot), S::kBufs * kW);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -226,147 +332,201 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   const uint32_t tmem_base = *tmem_slot;
   if (p.off) m_tiles = tabs.first[p.G];
   const int U = m_tiles * n_tiles;
+  // columns of part h that the MMAs take: a multiple of 32; 0 for a part behind column N
+  auto part_cols = [&](const Fp8Job& j, int h) { return min(kW, max(0, p.N - j.n0 - h * kW + 31) & ~31); };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RegsCopy));
+    if (warp == 0) {
       // ---------------- copies (both CTAs) ----------------
-      uint32_t it = 0;
-      bool ok = true;
+      uint32_t issued = 0, s = 0, phase = 1;
       const uint64_t pol_a = l2_policy_evict_last(), pol_b = l2_policy_evict_first();
+      const uint32_t free_bar = acc_full + 8 * (kH - 1) * S::kStages;
+      const uint32_t lead_bar = mapa_shared(full, 0);
+      const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
       auto a_box = [&](int rows) { return rows <= 0 ? -1 : (rows <= 16 ? 0 : (rows <= 64 ? 1 : 2)); };
       auto a_bytes = [&](int box) { return box < 0 ? 0u : (box == 0 ? 16u : (box == 1 ? 64u : 128u)) * 128u; };
-      for (int u = pair; u < U && ok; u += pairs) {
-        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kBN);
+      for (int u = pair; u < U && !*dead; u += pairs) {
+        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
         const int mine = a_box(j.row1 - (j.row0 + (int)rank * 128));
-        const int n_mma = min(kBN, (p.N - j.n0 + 31) & ~31);
-        const int bb = n_mma <= kBN / 2 ? 0 : 1;
-        const uint32_t tx = a_bytes(a_box(j.row1 - j.row0)) + a_bytes(a_box(j.row1 - j.row0 - 128)) +
-                            2u * (uint32_t)(bb ? kBN / 2 : kBN / 4) * 128u;
+        uint32_t tx = a_bytes(a_box(j.row1 - j.row0)) + a_bytes(a_box(j.row1 - j.row0 - 128));
+        int box[kH], yB[kH];
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const int n = part_cols(j, h);
+          box[h] = n == 0 ? -1 : (n <= kW / 2 ? 0 : 1);  // kW / 4 or kW / 2 rows from each CTA
+          yB[h] = j.group * p.N + j.n0 + h * kW + (int)rank * (n >> 1);
+          if (box[h] >= 0) tx += 2u * (uint32_t)(kW / (box[h] ? 2 : 4)) * 128u;
+        }
         const int yA = j.row0 + (int)rank * 128;
-        const int yB = j.group * p.N + j.n0 + (int)rank * (n_mma >> 1);
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
-          const int s = it % S::kStages;
-          if (!mbar_wait(smem_u32(&empty[s]), ((it / S::kStages) & 1) ^ 1, nullptr)) { ok = false; break; }
-          const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), tx);
-          if (mine >= 0) tma_load_2d_pair(smem_u32(sA + s * S::kStageA), &maps.a[mine], fb, kb * 128, yA, pol_a);
-          tma_load_2d_pair(smem_u32(sB + s * S::kStageB), &maps.b[bb], fb, kb * 128, yB, pol_b);
+#pragma unroll 1
+        for (int kb = 0; kb < p.KB; ++kb) {
+          wait_or_die(free_bar + s * 8u, phase, dead);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(full + s * 8u, tx);
+            if (mine >= 0) tma_load_2d_pair(dstA + s * S::kStageA, &maps.a[mine], lead_bar + s * 8u, kb * 128, yA, pol_a);
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+              if (box[h] >= 0)
+                tma_load_2d_pair(dstB + (s * kH + h) * S::kPartB, &maps.b[box[h]], lead_bar + s * 8u, kb * 128, yB[h], pol_b);
+          }
+          __syncwarp();
+          ++issued;
+          if (++s == S::kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
       // the leader's full barriers count both CTAs' bytes: wait until all have landed
       if (rank == 0) {
-        const uint32_t first = it > (uint32_t)S::kStages ? it - S::kStages : 0;
-        for (uint32_t q = first; q < it; ++q) mbar_wait(smem_u32(&full[q % S::kStages]), (q / S::kStages) & 1, nullptr);
+        const uint32_t first = issued > (uint32_t)S::kStages ? issued - S::kStages : 0;
+        for (uint32_t q = first; q < issued; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ---------------- MMAs (leader) ----------------
-      uint32_t it = 0;
-      bool ok = true;
-      for (int u = pair; u < U && ok; u += pairs) {
-        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kBN);
-        const uint32_t idesc = idesc_e4m3_f32(256, min(kBN, (p.N - j.n0 + 31) & ~31));
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
-          const int s = it % S::kStages, b = it % S::kBufs;
-          if (!mbar_wait(smem_u32(&acc_empty[b]), ((it / S::kBufs) & 1) ^ 1, nullptr) ||
-              !mbar_wait(smem_u32(&full[s]), (it / S::kStages) & 1, nullptr)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * S::kStageA), b0 = smem_u32(sB + s * S::kStageB);
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ---------------- MMAs (leader) ----------------
+        uint32_t s = 0, phase = 0, b = 0, b_phase = 1;
+        const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
+        for (int u = pair; u < U && !*dead; u += pairs) {
+          const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
+          uint32_t idesc[kH];
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_e4m3_pair(tmem_base + (uint32_t)(b * kBN), sdesc_k128(a0 + kk * 32), sdesc_k128(b0 + kk * 32), idesc,
-                           kk > 0 ? 1u : 0u);
-          umma_commit_pair_mc(smem_u32(&empty[s]), (uint16_t)3);
-          umma_commit_pair_mc(smem_u32(&acc_full[b]), (uint16_t)3);
+          for (int h = 0; h < kH; ++h) idesc[h] = part_cols(j, h) > 0 ? idesc_e4m3_f32(256, part_cols(j, h)) : 0u;
+#pragma unroll 1
+          for (int kb = 0; kb < p.KB; ++kb) {
+            wait_or_die(full + s * 8u, phase, dead);
+            const uint64_t da = descA + s * (S::kStageA / 16);
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+              wait_or_die(acc_empty + b * 8u, b_phase, dead);
+              tc_fence_after();
+              if (elect_one()) {
+                if (idesc[h] != 0u) {
+                  const uint64_t db = descB + (s * kH + h) * (S::kPartB / 16);
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
+                    umma_e4m3_pair(tmem_base + b * kW, da + 2 * kk, db + 2 * kk, idesc[h], kk > 0 ? 1u : 0u);
+                }
+                umma_commit_pair_mc(acc_full + (h * S::kStages + s) * 8u, (uint16_t)3);
+              }
+              __syncwarp();
+              if (++b == S::kBufs) {
+                b = 0;
+                b_phase ^= 1;
+              }
+            }
+            if (++s == S::kStages) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        if (elect_one()) umma_commit_pair(drain);
+        wait_or_die(drain, 0, dead);
+      }
+    } else if (warp == 2) {
+      // ---------------- scales (both CTAs) ----------------
+      // Four blocks at a time, up to four slots ahead of the epilogue: a load queues
+      // behind the copies of every stage, so it has to be issued early.
+      uint32_t slot = 0, phase = 1;
+      for (int u = pair; u < U && !*dead; u += pairs) {
+        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
+        const int row = j.row0 + (int)rank * 128 + lane;
+        const int blk = min((j.n0 + (lane % kH) * kW) / kFp8Block, p.NB - 1);
+        const float* const sb = p.sb + ((long long)j.group * p.NB + blk) * p.KB;
+#pragma unroll 1
+        for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
+          float v[4][4], vb = 0.f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* const src = p.sa + (long long)min(kb0 + q, p.KB - 1) * p.lds;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[q][i] = row + 32 * i < j.row1 ? __ldg(src + row + 32 * i) : 0.f;
+          }
+          if (lane < 4 * kH) vb = __ldg(sb + min(kb0 + lane / kH, p.KB - 1));
+          wait_or_die(sc_empty + slot * 8u, phase, dead);
+          float* const dst = s_scale + slot * S::kScaleSlot;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[q * 128 + 32 * i + lane] = v[q][i];
+          if (lane < 4 * kH) dst[4 * 128 + lane] = vb;
+          mbar_arrive(sc_full + slot * 8u);
+          if (++slot == S::kScaleSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-      umma_commit_pair(smem_u32(drain));
-      mbar_wait(smem_u32(drain), 0, nullptr);
     }
   } else {
-    // ---------------- epilogue (both CTAs; warps 2..9) ----------------
-    const int quarter = warp & 3;              // tensor-memory lanes [32 quarter, +32)
-    const int c_first = ((warp - 2) >> 2) * kHalf;  // columns [c_first, +kHalf)
+    // ---------------- epilogue (both CTAs; warps 4..11) ----------------
+    // Two warps per scheduler share this loop's latency, so little happens between
+    // a barrier and the next load: one wait, two loads and one arrival per part.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegsEpi));
+    const int ew = warp - 4, quarter = warp & 3;  // tensor-memory lanes [32 quarter, +32)
+    const int c_first = (ew >> 2) * kHalf;        // columns [c_first, +kHalf) of each part
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c_first;
-    const uint32_t release_to = mapa_shared(smem_u32(&acc_empty[0]), 0);
-    uint32_t it = 0;
-    bool ok = true;
+    const uint32_t release_to = mapa_shared(acc_empty, 0);
+    uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0;
     for (int u = pair; u < U; u += pairs) {
-      const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kBN);
+      const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
-      const int row = row_w0 + lane;
-      const int n_left = p.N - (j.n0 + c_first);  // valid columns of this warp (may exceed kHalf)
-      const bool work = row_w0 < j.row1 && n_left > 0;
-      uint64_t acc[kHalf / 2];
+      uint64_t acc[kH][kHalf / 2];
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0ull;
-      // the scales of the next kAhead blocks are on their way
-      const float* const sa = p.sa + min(row, j.row1 - 1);
-      const float* const sb = p.sb + ((long long)j.group * p.NB + min((j.n0 + c_first) / kFp8Block, p.NB - 1)) * p.KB;
-      float na[kAhead], nb[kAhead];
+      for (int h = 0; h < kH; ++h)
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        const int kb = min(q, p.KB - 1);
-        na[q] = __ldg(sa + (long long)kb * p.lds);
-        nb[q] = __ldg(sb + kb);
-      }
+        for (int i = 0; i < kHalf / 2; ++i) acc[h][i] = 0ull;
 #pragma unroll 1
       for (int kb = 0; kb < p.KB; ++kb) {
-        const float sc = na[0] * nb[0];
+        if ((kb & 3) == 0) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+        const float* const src = s_scale + slot * S::kScaleSlot + (kb & 3) * 128;
+        const float sav = src[quarter * 32 + lane];
+        uint64_t s2[kH];
 #pragma unroll
-        for (int q = 0; q + 1 < kAhead; ++q) {
-          na[q] = na[q + 1];
-          nb[q] = nb[q + 1];
+        for (int h = 0; h < kH; ++h) s2[h] = pack2(sav * s_scale[slot * S::kScaleSlot + 4 * 128 + (kb & 3) * kH + h]);
+        if ((kb & 3) == 3 || kb + 1 == p.KB) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+          if (++slot == S::kScaleSlots) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
         }
-        {
-          const int kn = min(kb + kAhead, p.KB - 1);
-          na[kAhead - 1] = __ldg(sa + (long long)kn * p.lds);
-          nb[kAhead - 1] = __ldg(sb + kn);
-        }
-        const int b = it % S::kBufs;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[b]), (it / S::kBufs) & 1, nullptr)) != 0;
-        ++it;
-        if (!ok) continue;
-        tc_fence_after();
-        if (work) {
-          const uint32_t t0 = lane_base + (uint32_t)(b * kBN);
-          const uint64_t s2 = pack2(sc);
-          uint32_t ra[16], rb[16];
-          tmem_ld16_nowait(t0, ra);
-          tmem_wait_ld16(ra);
 #pragma unroll
-          for (int c = 0; c < kHalf / 16; c += 2) {
-            tmem_ld16_nowait(t0 + (c + 1) * 16, rb);
+        for (int h = 0; h < kH; ++h) {
+          wait_or_die(acc_full + (h * S::kStages + s) * 8u, s_phase, dead);
+          tc_fence_after();
+          if (row_w0 < j.row1 && j.n0 + h * kW + c_first < p.N) {
+            const uint32_t t0 = lane_base + b * kW;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], ra[2 * i], ra[2 * i + 1], s2);
-            tmem_wait_ld16(rb);
-            if (c + 2 < kHalf / 16) tmem_ld16_nowait(t0 + (c + 2) * 16, ra);
+            for (int c = 0; c < kHalf / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32_nowait(t0 + c * 32, r);
+              tmem_wait32(r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fma2(acc[(c + 1) * 8 + i], rb[2 * i], rb[2 * i + 1], s2);
-            if (c + 2 < kHalf / 16) tmem_wait_ld16(ra);
+              for (int i = 0; i < 16; ++i) fma2(acc[h][c * 16 + i], r[2 * i], r[2 * i + 1], s2[h]);
+            }
           }
           tc_fence_before();
+          if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
+          b = (b + 1) % S::kBufs;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_peer(release_to + (uint32_t)b * 8u);
+        if (++s == S::kStages) {
+          s = 0;
+          s_phase ^= 1;
+        }
       }
-      if (work && row < j.row1) {
-        const float w = !ok ? __uint_as_float(0x7fffffffu) : (p.row_w ? __ldg(p.row_w + row) : 1.0f);
-        TO* const o = static_cast<TO*>(p.out) + (long long)row * p.ldo + j.n0 + c_first;
+      const int row = row_w0 + lane;
+      // a wait that ran out: what was added is not the product
+      const float w = *dead ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
 #pragma unroll
-        for (int c = 0; c < kHalf / 8; ++c) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float((uint32_t)acc[c * 4 + i]) * w;
-            v[2 * i + 1] = __uint_as_float((uint32_t)(acc[c * 4 + i] >> 32)) * w;
-          }
-          if (c * 8 < n_left) store8(o + c * 8, v, n_left - c * 8, p.vec_out != 0);
-        }
+      for (int h = 0; h < kH; ++h) {
+        const int col = j.n0 + h * kW + c_first;
+        if (row_w0 < j.row1 && col < p.N)
+          store_turned<TO, kHalf>(s_turn + ew * 4096, static_cast<TO*>(p.out) + (long long)row_w0 * p.ldo + col, p.ldo,
+                                  acc[h], w, lane, min(32, j.row1 - row_w0), p.N - col, p.vec_out != 0);
       }
     }
   }
@@ -375,7 +535,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   __syncthreads();
   cluster_sync_all();  // the pair's MMAs, copies and tensor-memory reads are all done
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem_base, S::kBufs * kBN);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, S::kBufs * kW);
   __syncthreads();
   cluster_sync_all();
 }
