@@ -33,7 +33,7 @@
 //   full[s]         rank 0's: both CTAs' copies of a stage have landed
 //   acc_full[h][s]  both: part h's sums of the stage's block are in tensor
 //                   memory; the last part's also frees the stage
-//   acc_empty[b]    rank 0's: all 16 epilogue warps have read the buffer
+//   acc_empty[b]    rank 0's: the epilogue warps of both CTAs have read the buffer
 //   sc_full, sc_empty[i]  each CTA's own: a slot of scales is written, is read
 // All waits are bounded; after one runs out the CTA stops working and stores
 // NaN for what it could not compute.
@@ -192,6 +192,8 @@ struct Fp8Shape {
   static constexpr int kStages = kBN >= 256 ? 5 : (kBN >= 128 ? 6 : 8);
   static constexpr int kStageA = 128 * 128, kPartB = (kW / 2) * 128, kStage = kStageA + kH * kPartB;
   static constexpr int kTurn = kFp8EpiWarps * 4096;  // 32 rows x 128 bytes per warp
+  static constexpr int kCols = kH == 2 ? kW : kW / 2;  // columns of an epilogue warp
+  static constexpr int kReaders = kH == 2 ? kFp8EpiWarps / 2 : kFp8EpiWarps;  // warps of a CTA that read a buffer
   // row and weight scales of four blocks per slot: [4][128] and [4][kH] floats
   static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * kH;
   static constexpr int kBars = kStages * (1 + kH) + kBufs + 2 * kScaleSlots + 1;
@@ -254,7 +256,6 @@ template <int kW, int kH, class TO>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8GemmParams p) {
   using S = Fp8Shape<kW, kH>;
-  constexpr int kHalf = kW / 2;  // columns of each part that an epilogue warp takes
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Fp8Tables tabs;
   __shared__ int s_dead;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       mbar_init(full + 8 * s, 1);
       for (int h = 0; h < kH; ++h) mbar_init(acc_full + 8 * (h * S::kStages + s), 1);
     }
-    for (int b = 0; b < S::kBufs; ++b) mbar_init(acc_empty + 8 * b, 2 * kFp8EpiWarps);
+    for (int b = 0; b < S::kBufs; ++b) mbar_init(acc_empty + 8 * b, 2 * S::kReaders);
     for (int i = 0; i < S::kScaleSlots; ++i) {
       mbar_init(sc_full + 8 * i, 32);
       mbar_init(sc_empty + 8 * i, kFp8EpiWarps);
@@ -462,30 +463,30 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     }
   } else {
     // ---------------- epilogue (both CTAs; warps 4..11) ----------------
-    // Two warps per scheduler share this loop's latency, so little happens between
-    // a barrier and the next load: one wait, two loads and one arrival per part.
+    // The two warps of a lane quarter take one part each (kH = 2), so that one adds
+    // while the other waits, or half of the only part's columns.  One wait, one
+    // arrival and one pair of scales per block: two warps per scheduler cannot
+    // hide more.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegsEpi));
     const int ew = warp - 4, quarter = warp & 3;  // tensor-memory lanes [32 quarter, +32)
-    const int c_first = (ew >> 2) * kHalf;        // columns [c_first, +kHalf) of each part
-    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c_first;
-    const uint32_t release_to = mapa_shared(acc_empty, 0);
+    const int h = kH == 2 ? ew >> 2 : 0;
+    const int c_first = kH == 2 ? 0 : (ew >> 2) * S::kCols;  // columns [c_first, +kCols) of part h
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(h * kW + c_first);
+    const uint32_t release_to = mapa_shared(acc_empty, 0) + (uint32_t)h * 8u;
+    const uint32_t my_full = acc_full + 8u * (uint32_t)(h * S::kStages);
     uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0;
     for (int u = pair; u < U; u += pairs) {
       const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
-      uint64_t acc[kH][kHalf / 2];
-#pragma unroll
-      for (int h = 0; h < kH; ++h)
-#pragma unroll
-        for (int i = 0; i < kHalf / 2; ++i) acc[h][i] = 0ull;
-#pragma unroll 1
-      for (int kb = 0; kb < p.KB; ++kb) {
+      const int col = j.n0 + h * kW + c_first;
+      const bool work = row_w0 < j.row1 && col < p.N;
+      float sav = 0.f, sbv = 0.f;  // the scales of the next block
+      auto next_scales = [&](int kb) {
+        if (kb >= p.KB) return;
         if ((kb & 3) == 0) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-        const float* const src = s_scale + slot * S::kScaleSlot + (kb & 3) * 128;
-        const float sav = src[quarter * 32 + lane];
-        uint64_t s2[kH];
-#pragma unroll
-        for (int h = 0; h < kH; ++h) s2[h] = pack2(sav * s_scale[slot * S::kScaleSlot + 4 * 128 + (kb & 3) * kH + h]);
+        const float* const src = s_scale + slot * S::kScaleSlot;
+        sav = src[(kb & 3) * 128 + quarter * 32 + lane];
+        sbv = src[4 * 128 + (kb & 3) * kH + h];
         if ((kb & 3) == 3 || kb + 1 == p.KB) {
           __syncwarp();
           if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
@@ -494,25 +495,33 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             slot_phase ^= 1;
           }
         }
+      };
+      uint64_t acc[S::kCols / 2];
 #pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          wait_or_die(acc_full + (h * S::kStages + s) * 8u, s_phase, dead);
-          tc_fence_after();
-          if (row_w0 < j.row1 && j.n0 + h * kW + c_first < p.N) {
-            const uint32_t t0 = lane_base + b * kW;
+      for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0ull;
+      next_scales(0);
+#pragma unroll 1
+      for (int kb = 0; kb < p.KB; ++kb) {
+        const uint64_t s2 = pack2(sav * sbv);
+        wait_or_die(my_full + s * 8u, s_phase, dead);
+        tc_fence_after();
+        const uint32_t t0 = lane_base + b * kW;
+        uint32_t r[2][32];
+        if (work) tmem_ld32_nowait(t0, r[0]);
+        next_scales(kb + 1);
+        if (work) {
+          tmem_wait32(r[0]);
 #pragma unroll
-            for (int c = 0; c < kHalf / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32_nowait(t0 + c * 32, r);
-              tmem_wait32(r);
+          for (int c = 0; c < S::kCols / 32; ++c) {
+            if (c + 1 < S::kCols / 32) tmem_ld32_nowait(t0 + (c + 1) * 32, r[(c + 1) & 1]);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) fma2(acc[h][c * 16 + i], r[2 * i], r[2 * i + 1], s2[h]);
-            }
+            for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s2);
+            if (c + 1 < S::kCols / 32) tmem_wait32(r[(c + 1) & 1]);
           }
-          tc_fence_before();
-          if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
-          b = (b + 1) % S::kBufs;
         }
+        tc_fence_before();
+        if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
+        b = (b + kH) % S::kBufs;
         if (++s == S::kStages) {
           s = 0;
           s_phase ^= 1;
@@ -521,13 +530,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       const int row = row_w0 + lane;
       // a wait that ran out: what was added is not the product
       const float w = *dead ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
-#pragma unroll
-      for (int h = 0; h < kH; ++h) {
-        const int col = j.n0 + h * kW + c_first;
-        if (row_w0 < j.row1 && col < p.N)
-          store_turned<TO, kHalf>(s_turn + ew * 4096, static_cast<TO*>(p.out) + (long long)row_w0 * p.ldo + col, p.ldo,
-                                  acc[h], w, lane, min(32, j.row1 - row_w0), p.N - col, p.vec_out != 0);
-      }
+      if (work)
+        store_turned<TO, S::kCols>(s_turn + ew * 4096, static_cast<TO*>(p.out) + (long long)row_w0 * p.ldo + col, p.ldo,
+                                   acc, w, lane, min(32, j.row1 - row_w0), p.N - col, p.vec_out != 0);
     }
   }
 
