@@ -131,17 +131,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
-// acc (two fp32) += (lo, hi) * s (two equal fp32)
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(lo), "r"(hi), "l"(s));
-}
-__device__ __forceinline__ uint64_t pack2(float v) {
-  const uint32_t u = __float_as_uint(v);
-  return ((uint64_t)u << 32) | u;
-}
-
 // tensor maps: A with boxes of 16, 64 and 128 rows, B with boxes of kW / 4 and kW / 2 rows
 struct Fp8Maps {
   CUtensorMap a[3];
@@ -205,7 +194,7 @@ struct Fp8Shape {
 // units swizzled by row: both sides are free of bank conflicts.  Rows from
 // `rows` on and columns from `cols` on are not stored.
 template <class TO, int kCols>
-__device__ __forceinline__ void store_turned(uint8_t* turn, TO* out, long long ldo, const uint64_t* acc, float w,
+__device__ __forceinline__ void store_turned(uint8_t* turn, TO* out, long long ldo, const float* acc, float w,
                                              int lane, int rows, int cols, bool vec) {
   constexpr int kPer = 128 / (int)sizeof(TO);       // columns per pass
   constexpr int kPass = kCols < kPer ? kCols : kPer;
@@ -220,11 +209,9 @@ __device__ __forceinline__ void store_turned(uint8_t* turn, TO* out, long long l
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(TO) == 4) {
-          const uint64_t a = acc[(c0 + u * kUnit + i) >> 1];
-          x[i] = __float_as_uint(__uint_as_float((uint32_t)((i & 1) ? (a >> 32) : a)) * w);
+          x[i] = __float_as_uint(acc[c0 + u * kUnit + i] * w);
         } else {
-          const uint64_t a = acc[(c0 + u * kUnit + 2 * i) >> 1];
-          const float lo = __uint_as_float((uint32_t)a) * w, hi = __uint_as_float((uint32_t)(a >> 32)) * w;
+          const float lo = acc[c0 + u * kUnit + 2 * i] * w, hi = acc[c0 + u * kUnit + 2 * i + 1] * w;
           if constexpr (std::is_same_v<TO, __half>) x[i] = pack_f16x2(lo, hi);
           else x[i] = pack_bf16x2(lo, hi);
         }
@@ -496,37 +483,40 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           }
         }
       };
-      uint64_t acc[S::kCols / 2];
+      float acc[S::kCols];
 #pragma unroll
-      for (int i = 0; i < S::kCols / 2; ++i) acc[i] = 0ull;
+      for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
       next_scales(0);
+      auto blocks = [&](auto works) {
 #pragma unroll 1
-      for (int kb = 0; kb < p.KB; ++kb) {
-        const uint64_t s2 = pack2(sav * sbv);
-        wait_or_die(my_full + s * 8u, s_phase, dead);
-        tc_fence_after();
-        const uint32_t t0 = lane_base + b * kW;
-        uint32_t r[2][32];
-        if (work) tmem_ld32_nowait(t0, r[0]);
-        next_scales(kb + 1);
-        if (work) {
-          tmem_wait32(r[0]);
+        for (int kb = 0; kb < p.KB; ++kb) {
+          const float sc = sav * sbv;
+          next_scales(kb + 1);
+          wait_or_die(my_full + s * 8u, s_phase, dead);
+          tc_fence_after();
+          if constexpr (decltype(works)::value) {
+            const uint32_t t0 = lane_base + b * kW;
 #pragma unroll
-          for (int c = 0; c < S::kCols / 32; ++c) {
-            if (c + 1 < S::kCols / 32) tmem_ld32_nowait(t0 + (c + 1) * 32, r[(c + 1) & 1]);
+            for (int c = 0; c < S::kCols / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32_nowait(t0 + c * 32, r);
+              tmem_wait32(r);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s2);
-            if (c + 1 < S::kCols / 32) tmem_wait32(r[(c + 1) & 1]);
+              for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sc, acc[c * 32 + i]);
+            }
+          }
+          tc_fence_before();
+          if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
+          b = (b + kH) % S::kBufs;
+          if (++s == S::kStages) {
+            s = 0;
+            s_phase ^= 1;
           }
         }
-        tc_fence_before();
-        if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
-        b = (b + kH) % S::kBufs;
-        if (++s == S::kStages) {
-          s = 0;
-          s_phase ^= 1;
-        }
-      }
+      };
+      // two loops: a condition inside the loop cost a register move per loaded value
+      if (work) blocks(std::true_type{});
+      else      blocks(std::false_type{});
       const int row = row_w0 + lane;
       // a wait that ran out: what was added is not the product
       const float w = *dead ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
