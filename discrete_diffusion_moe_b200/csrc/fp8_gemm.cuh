@@ -32,7 +32,7 @@
 // Protocol of the barriers (rank 0 leads):
 //   full[s]         rank 0's: both CTAs' copies of a stage have landed
 //   acc_full[h][s]  both: part h's sums of the stage's block are in tensor
-//                   memory; the last part's also frees the stage
+//                   memory; those of all parts free the stage
 //   acc_empty[b]    rank 0's: the epilogue warps of both CTAs have read the buffer
 //   sc_full, sc_empty[i]  each CTA's own: a slot of scales is written, is read
 // All waits are bounded; after one runs out the CTA stops working and stores
@@ -48,7 +48,7 @@ namespace dg {
 
 constexpr int kFp8MaxGroups = 1024;
 constexpr int kFp8EpiWarps = 8;
-// Warpgroup 0: the copying warp, the MMA warp and two idle ones; warpgroups 1 and 2:
+// Warpgroup 0: a copying warp, two MMA warps, a scale warp; warpgroups 1 and 2:
 // the epilogue.  384 threads x 168 registers at launch; warpgroup 0 gives back what
 // the epilogue takes.  Nothing may spill: with nearly all of the SM's memory used
 // as shared memory a spilled register comes back from L2 (measured: 400 cycles a
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       mbar_init(sc_full + 8 * i, 32);
       mbar_init(sc_empty + 8 * i, kFp8EpiWarps);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     s_dead = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -329,7 +329,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // ---------------- copies (both CTAs) ----------------
       uint32_t issued = 0, s = 0, phase = 1;
       const uint64_t pol_a = l2_policy_evict_last(), pol_b = l2_policy_evict_first();
-      const uint32_t free_bar = acc_full + 8 * (kH - 1) * S::kStages;
       const uint32_t lead_bar = mapa_shared(full, 0);
       const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
       auto a_box = [&](int rows) { return rows <= 0 ? -1 : (rows <= 16 ? 0 : (rows <= 64 ? 1 : 2)); };
@@ -349,7 +348,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const int yA = j.row0 + (int)rank * 128;
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-          wait_or_die(free_bar + s * 8u, phase, dead);
+#pragma unroll
+          for (int h = 0; h < kH; ++h) wait_or_die(acc_full + (h * S::kStages + s) * 8u, phase, dead);
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s * 8u, tx);
             if (mine >= 0) tma_load_2d_pair(dstA + s * S::kStageA, &maps.a[mine], lead_bar + s * 8u, kb * 128, yA, pol_a);
@@ -371,44 +371,47 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const uint32_t first = issued > (uint32_t)S::kStages ? issued - S::kStages : 0;
         for (uint32_t q = first; q < issued; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
       if (rank == 0) {
         // ---------------- MMAs (leader) ----------------
-        uint32_t s = 0, phase = 0, b = 0, b_phase = 1;
-        const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
+        // Two warps take the parts (kH = 2) or the blocks (kH = 1) in turn: issuing a
+        // part's MMAs takes about as long as they run, and a ready barrier still
+        // answers after about 100 cycles, so one warp left the tensor cores idle
+        // half of the time (measured 1000 cycles per block of 512).
+        const int m = warp >> 1;
+        const int h = kH == 2 ? m : 0;
+        uint32_t s = kH == 2 ? 0 : m, phase = 0, b = m, b_phase = 1;
+        int skip = kH == 2 ? 0 : m;  // blocks until the next one of this warp
+        const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB)) + h * (S::kPartB / 16);
         for (int u = pair; u < U && !*dead; u += pairs) {
           const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
-          uint32_t idesc[kH];
-#pragma unroll
-          for (int h = 0; h < kH; ++h) idesc[h] = part_cols(j, h) > 0 ? idesc_e4m3_f32(256, part_cols(j, h)) : 0u;
+          const int n = part_cols(j, h);
+          const uint32_t idesc = idesc_e4m3_f32(256, n);
+          int kb = skip;
 #pragma unroll 1
-          for (int kb = 0; kb < p.KB; ++kb) {
+          for (; kb < p.KB; kb += 3 - kH) {
             wait_or_die(full + s * 8u, phase, dead);
-            const uint64_t da = descA + s * (S::kStageA / 16);
+            wait_or_die(acc_empty + b * 8u, b_phase, dead);
+            tc_fence_after();
+            if (elect_one()) {
+              if (n > 0) {
+                const uint64_t da = descA + s * (S::kStageA / 16), db = descB + s * (kH * S::kPartB / 16);
 #pragma unroll
-            for (int h = 0; h < kH; ++h) {
-              wait_or_die(acc_empty + b * 8u, b_phase, dead);
-              tc_fence_after();
-              if (elect_one()) {
-                if (idesc[h] != 0u) {
-                  const uint64_t db = descB + (s * kH + h) * (S::kPartB / 16);
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
-                    umma_e4m3_pair(tmem_base + b * kW, da + 2 * kk, db + 2 * kk, idesc[h], kk > 0 ? 1u : 0u);
-                }
-                umma_commit_pair_mc(acc_full + (h * S::kStages + s) * 8u, (uint16_t)3);
+                for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
+                  umma_e4m3_pair(tmem_base + b * kW, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
               }
-              __syncwarp();
-              if (++b == S::kBufs) {
-                b = 0;
-                b_phase ^= 1;
-              }
+              umma_commit_pair_mc(acc_full + (h * S::kStages + s) * 8u, (uint16_t)3);
             }
-            if (++s == S::kStages) {
-              s = 0;
+            __syncwarp();
+            b ^= 2u;
+            if (b == (uint32_t)m) b_phase ^= 1;
+            s += 3 - kH;
+            if (s >= S::kStages) {
+              s -= S::kStages;
               phase ^= 1;
             }
           }
+          skip = kb - p.KB;
         }
         if (elect_one()) umma_commit_pair(drain);
         wait_or_die(drain, 0, dead);
@@ -467,38 +470,42 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
       const int col = j.n0 + h * kW + c_first;
       const bool work = row_w0 < j.row1 && col < p.N;
-      float sav = 0.f, sbv = 0.f;  // the scales of the next block
-      auto next_scales = [&](int kb) {
-        if (kb >= p.KB) return;
-        if ((kb & 3) == 0) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-        const float* const src = s_scale + slot * S::kScaleSlot;
-        sav = src[(kb & 3) * 128 + quarter * 32 + lane];
-        sbv = src[4 * 128 + (kb & 3) * kH + h];
-        if ((kb & 3) == 3 || kb + 1 == p.KB) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
-          if (++slot == S::kScaleSlots) {
-            slot = 0;
-            slot_phase ^= 1;
-          }
-        }
-      };
       float acc[S::kCols];
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
-      next_scales(0);
+      // the scales of the next block: read while this one is added (from the last
+      // block on the same slot is read again, unused)
+      wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+      const float* my_sa = s_scale + slot * S::kScaleSlot + quarter * 32 + lane;
+      const float* my_sb = s_scale + slot * S::kScaleSlot + 4 * 128 + h;
+      float sav = my_sa[0], sbv = my_sb[0];
       auto blocks = [&](auto works) {
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
           const float sc = sav * sbv;
-          next_scales(kb + 1);
           wait_or_die(my_full + s * 8u, s_phase, dead);
           tc_fence_after();
+          const uint32_t t0 = lane_base + b * kW;
+          uint32_t r[32];
+          if constexpr (decltype(works)::value) tmem_ld32_nowait(t0, r);
+          if ((kb & 3) == 3 || kb + 1 == p.KB) {  // this slot has been read
+            if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+            if (++slot == S::kScaleSlots) {
+              slot = 0;
+              slot_phase ^= 1;
+            }
+            if (kb + 1 < p.KB) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+            my_sa = s_scale + slot * S::kScaleSlot + quarter * 32 + lane;
+            my_sb = s_scale + slot * S::kScaleSlot + 4 * 128 + h;
+          }
+          sav = my_sa[((kb + 1) & 3) * 128];
+          sbv = my_sb[((kb + 1) & 3) * kH];
           if constexpr (decltype(works)::value) {
-            const uint32_t t0 = lane_base + b * kW;
+            tmem_wait32(r);
 #pragma unroll
-            for (int c = 0; c < S::kCols / 32; ++c) {
-              uint32_t r[32];
+            for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), sc, acc[i]);
+#pragma unroll
+            for (int c = 1; c < S::kCols / 32; ++c) {
               tmem_ld32_nowait(t0 + c * 32, r);
               tmem_wait32(r);
 #pragma unroll
