@@ -1,6 +1,7 @@
 // fp8_api.cu - host side of the 8-bit block-scaled operators of include/dg.h:
 // argument checks, choice of kernel and launches.
 #include <stdint.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -74,6 +75,25 @@ dg_status make_tmap_codes(CUtensorMap* m, const uint8_t* base, long long K, long
   return DG_OK;
 }
 
+// The output [M, N] for stores of boxes of 128 bytes x 32 rows with the 128-byte
+// swizzle, clipped at its edges.
+template <class TO>
+dg_status make_tmap_out(CUtensorMap* m, void* base, long long N, long long M, long long ldo) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const CUtensorMapDataType dt = std::is_same_v<TO, float> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : std::is_same_v<TO, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+  cuuint64_t strides[1] = {(cuuint64_t)ldo * sizeof(TO)};
+  cuuint32_t box[2] = {128 / sizeof(TO), 32};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = fn(m, dt, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DG_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return DG_OK;
+}
+
 template <int kW, int kH, class TO>
 dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
   using S = Fp8Shape<kW, kH>;
@@ -81,6 +101,8 @@ dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
   const int a_rows[3] = {16, 64, 128};
   for (int i = 0; i < 3; ++i) DG_TRY(make_tmap_codes(&maps.a[i], p.a, p.K, p.M, p.lda, a_rows[i]));
   for (int i = 0; i < 2; ++i) DG_TRY(make_tmap_codes(&maps.b[i], p.b, p.K, (long long)p.G * p.N, p.ldb, kW / (i ? 2 : 4)));
+  memset(&maps.out, 0, sizeof maps.out);
+  if (p.vec_out) DG_TRY(make_tmap_out<TO>(&maps.out, p.out, p.N, p.M, p.ldo));
   const void* fn = (const void*)fp8_pair_kernel<kW, kH, TO>;
   DG_TRY(set_smem_attr(fn, S::kSmem, true));
   const long long tiles = p.off ? std::min(p.G, p.M) + (long long)p.M / 256 : ceil_div(p.M, 256);  // at most

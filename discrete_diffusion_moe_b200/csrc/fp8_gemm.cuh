@@ -82,6 +82,18 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Whether the phase of parity `parity` has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Bounded wait without a result: when it runs out, *dead is set (then later waits
 // end at once) and the caller goes on; the kernel's results are marked at their
 // store.  Warps are converged again after it.
@@ -132,9 +144,11 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 // tensor maps: A with boxes of 16, 64 and 128 rows, B with boxes of kW / 4 and kW / 2 rows
+// and the output with boxes of 128 bytes x 32 rows (when its rows are 16-byte aligned)
 struct Fp8Maps {
   CUtensorMap a[3];
   CUtensorMap b[2];
+  CUtensorMap out;
 };
 
 struct Fp8Tables {
@@ -178,64 +192,85 @@ template <int kW, int kH>
 struct Fp8Shape {
   static constexpr int kBN = kW * kH;
   static constexpr int kBufs = 4;  // tensor-memory buffers of kW columns
-  static constexpr int kStages = kBN >= 256 ? 5 : (kBN >= 128 ? 6 : 8);
+  static constexpr int kStages = kBN >= 256 ? 4 : (kBN >= 128 ? 5 : 6);
   static constexpr int kStageA = 128 * 128, kPartB = (kW / 2) * 128, kStage = kStageA + kH * kPartB;
-  static constexpr int kTurn = kFp8EpiWarps * 4096;  // 32 rows x 128 bytes per warp
+  static constexpr int kTurn = kFp8EpiWarps * 8192;  // two buffers of 32 rows x 128 bytes per warp
   static constexpr int kCols = kH == 2 ? kW : kW / 2;  // columns of an epilogue warp
   static constexpr int kReaders = kH == 2 ? kFp8EpiWarps / 2 : kFp8EpiWarps;  // warps of a CTA that read a buffer
-  // row and weight scales of four blocks per slot: [4][128] and [4][kH] floats
+  // row and weight scales of four blocks per slot: [128][4] and [kH][4] floats
   static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * kH;
   static constexpr int kBars = kStages * (1 + kH) + kBufs + 2 * kScaleSlots + 1;
   static constexpr int kSmem = 1024 + kStages * kStage + kTurn + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
 };
 
-// Stores a warp's 32 rows x kCols results (thread `lane` holds row lane in v)
-// through its 4 KB of shared memory, 128 bytes of each row at a time, 16-byte
-// units swizzled by row: both sides are free of bank conflicts.  Rows from
-// `rows` on and columns from `cols` on are not stored.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src), "r"(x),
+               "r"(y)
+               : "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+
+// Stores a warp's 32 rows x kCols results (thread `lane` holds row lane in acc),
+// 128 bytes of each row at a time, through its two 4 KB buffers of shared memory
+// with the 128-byte swizzle (16-byte units by row): free of bank conflicts on
+// both sides.  With a tensor map the copy engine does the global side while the
+// warp goes on (columns from the matrix's end on are clipped); else the warp
+// stores whole rows itself: rows [0, rows), columns [0, cols).
 template <class TO, int kCols>
-__device__ __forceinline__ void store_turned(uint8_t* turn, TO* out, long long ldo, const float* acc, float w,
-                                             int lane, int rows, int cols, bool vec) {
-  constexpr int kPer = 128 / (int)sizeof(TO);       // columns per pass
+__device__ __forceinline__ void store_turned(uint8_t* turn, const CUtensorMap* map, int x, int y, TO* out, long long ldo,
+                                             const float* acc, float w, int lane, int rows, int cols, bool vec) {
+  constexpr int kPer = 128 / (int)sizeof(TO);  // columns per pass
   constexpr int kPass = kCols < kPer ? kCols : kPer;
-  constexpr int kUnit = 16 / (int)sizeof(TO);       // columns per 16-byte unit
-  constexpr int kUnits = kPass / kUnit;
+  constexpr int kUnit = 16 / (int)sizeof(TO);  // columns per 16-byte unit
 #pragma unroll
   for (int c0 = 0; c0 < kCols; c0 += kPass) {
     if (c0 >= cols) break;
+    uint8_t* const buf = turn + ((c0 / kPass) & 1) * 4096;
+    if (lane == 0) bulk_wait_read<1>();  // what this buffer held has been read
+    __syncwarp();
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      uint32_t x[4];
+    for (int u = 0; u < kPass / kUnit; ++u) {
+      uint32_t v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(TO) == 4) {
-          x[i] = __float_as_uint(acc[c0 + u * kUnit + i] * w);
+          v[i] = __float_as_uint(acc[c0 + u * kUnit + i] * w);
         } else {
           const float lo = acc[c0 + u * kUnit + 2 * i] * w, hi = acc[c0 + u * kUnit + 2 * i + 1] * w;
-          if constexpr (std::is_same_v<TO, __half>) x[i] = pack_f16x2(lo, hi);
-          else x[i] = pack_bf16x2(lo, hi);
+          if constexpr (std::is_same_v<TO, __half>) v[i] = pack_f16x2(lo, hi);
+          else v[i] = pack_bf16x2(lo, hi);
         }
       }
-      *reinterpret_cast<uint4*>(turn + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    __syncwarp();
-    if (vec && c0 + kPass <= cols) {
-      constexpr int kRowsPer = 32 / kUnits;  // rows per store instruction
-      const int u = lane % kUnits;
-#pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += kRowsPer) {
-        const int r = r0 + lane / kUnits;
-        const uint4 q = *reinterpret_cast<const uint4*>(turn + r * 128 + ((u ^ (r & 7)) * 16));
-        if (r < rows) *reinterpret_cast<uint4*>(out + r * ldo + c0 + u * kUnit) = q;
+    if (map) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(map, smem_u32(buf), x + c0, y);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     } else {
+      __syncwarp();
       const int n = min(kPass, cols - c0);
-      for (int r = 0; r < rows; ++r)
+      constexpr int kUnits = kPass / kUnit;
+      if (vec && n == kPass) {
+        const int u = lane % kUnits;
+        for (int r = lane / kUnits; r < rows; r += 32 / kUnits)
+          *reinterpret_cast<uint4*>(out + r * ldo + c0 + u * kUnit) =
+              *reinterpret_cast<const uint4*>(buf + r * 128 + ((u ^ (r & 7)) * 16));
+      } else {
+        for (int r = 0; r < rows; ++r)
         for (int c = lane; c < n; c += 32)
           out[r * ldo + c0 + c] =
-              *reinterpret_cast<const TO*>(turn + r * 128 + (((c / kUnit) ^ (r & 7)) * 16) + (c % kUnit) * sizeof(TO));
+              *reinterpret_cast<const TO*>(buf + r * 128 + (((c / kUnit) ^ (r & 7)) * 16) + (c % kUnit) * sizeof(TO));
+      }
+      if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // keeps the count of passes
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
@@ -424,7 +459,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       for (int u = pair; u < U && !*dead; u += pairs) {
         const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
         const int row = j.row0 + (int)rank * 128 + lane;
-        const int blk = min((j.n0 + (lane % kH) * kW) / kFp8Block, p.NB - 1);
+        const int blk = min((j.n0 + min(lane >> 2, kH - 1) * kW) / kFp8Block, p.NB - 1);
         const float* const sb = p.sb + ((long long)j.group * p.NB + blk) * p.KB;
 #pragma unroll 1
         for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
@@ -435,13 +470,12 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[q][i] = row + 32 * i < j.row1 ? __ldg(src + row + 32 * i) : 0.f;
           }
-          if (lane < 4 * kH) vb = __ldg(sb + min(kb0 + lane / kH, p.KB - 1));
+          if (lane < 4 * kH) vb = __ldg(sb + min(kb0 + (lane & 3), p.KB - 1));
           wait_or_die(sc_empty + slot * 8u, phase, dead);
           float* const dst = s_scale + slot * S::kScaleSlot;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[q * 128 + 32 * i + lane] = v[q][i];
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(dst)[32 * i + lane] = make_float4(v[0][i], v[1][i], v[2][i], v[3][i]);
           if (lane < 4 * kH) dst[4 * 128 + lane] = vb;
           mbar_arrive(sc_full + slot * 8u);
           if (++slot == S::kScaleSlots) {
@@ -473,33 +507,47 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       float acc[S::kCols];
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
-      // the scales of the next block: read while this one is added (from the last
-      // block on the same slot is read again, unused)
-      wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-      const float* my_sa = s_scale + slot * S::kScaleSlot + quarter * 32 + lane;
-      const float* my_sb = s_scale + slot * S::kScaleSlot + 4 * 128 + h;
-      float sav = my_sa[0], sbv = my_sb[0];
+      // scales of four blocks (sc4); those of the next four are read a block early
+      float4 sa4, sb4;
+      auto read_scales = [&]() {
+        wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+        const float4* const src = reinterpret_cast<const float4*>(s_scale + slot * S::kScaleSlot);
+        sa4 = src[quarter * 32 + lane];
+        sb4 = src[128 + h];
+      };
+      auto free_scales = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+        if (++slot == S::kScaleSlots) {
+          slot = 0;
+          slot_phase ^= 1;
+        }
+      };
+      read_scales();
       auto blocks = [&](auto works) {
+        float4 sc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool ready = mbar_test_wait(my_full + s * 8u, s_phase);
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-          const float sc = sav * sbv;
-          wait_or_die(my_full + s * 8u, s_phase, dead);
+          const int q = kb & 3;
+          if (q == 0) {
+            sc4 = make_float4(sa4.x * sb4.x, sa4.y * sb4.y, sa4.z * sb4.z, sa4.w * sb4.w);
+            free_scales();
+          }
+          const float sc = q < 2 ? (q == 0 ? sc4.x : sc4.y) : (q == 2 ? sc4.z : sc4.w);
+          if (!ready) wait_or_die(my_full + s * 8u, s_phase, dead);
+          __syncwarp();
           tc_fence_after();
           const uint32_t t0 = lane_base + b * kW;
           uint32_t r[32];
           if constexpr (decltype(works)::value) tmem_ld32_nowait(t0, r);
-          if ((kb & 3) == 3 || kb + 1 == p.KB) {  // this slot has been read
-            if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
-            if (++slot == S::kScaleSlots) {
-              slot = 0;
-              slot_phase ^= 1;
-            }
-            if (kb + 1 < p.KB) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-            my_sa = s_scale + slot * S::kScaleSlot + quarter * 32 + lane;
-            my_sb = s_scale + slot * S::kScaleSlot + 4 * 128 + h;
+          if (++s == S::kStages) {
+            s = 0;
+            s_phase ^= 1;
           }
-          sav = my_sa[((kb + 1) & 3) * 128];
-          sbv = my_sb[((kb + 1) & 3) * kH];
+          // the next block's barrier is asked while this block is added (behind the
+          // last block it is the next unit's first)
+          ready = mbar_test_wait(my_full + s * 8u, s_phase);
           if constexpr (decltype(works)::value) {
             tmem_wait32(r);
 #pragma unroll
@@ -515,10 +563,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           tc_fence_before();
           if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
           b = (b + kH) % S::kBufs;
-          if (++s == S::kStages) {
-            s = 0;
-            s_phase ^= 1;
-          }
+          if (q == 2 && kb + 2 < p.KB) read_scales();
         }
       };
       // two loops: a condition inside the loop cost a register move per loaded value
@@ -527,10 +572,15 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       const int row = row_w0 + lane;
       // a wait that ran out: what was added is not the product
       const float w = *dead ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
+      // the copy engine clips at the matrix's edges only, not at a group's last row
+      const int rows = min(32, j.row1 - row_w0);
+      const bool whole = S::kCols * sizeof(TO) >= 128 && p.vec_out && (rows == 32 || !p.off);
       if (work)
-        store_turned<TO, S::kCols>(s_turn + ew * 4096, static_cast<TO*>(p.out) + (long long)row_w0 * p.ldo + col, p.ldo,
-                                   acc, w, lane, min(32, j.row1 - row_w0), p.N - col, p.vec_out != 0);
+        store_turned<TO, S::kCols>(s_turn + ew * 8192, whole ? &maps.out : nullptr, col, row_w0,
+                                   static_cast<TO*>(p.out) + (long long)row_w0 * p.ldo + col, p.ldo, acc, w, lane, rows,
+                                   p.N - col, p.vec_out != 0);
     }
+    if (lane == 0) bulk_wait_read<0>();
   }
 
   tc_fence_before();
