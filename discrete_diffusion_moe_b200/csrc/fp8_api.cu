@@ -94,20 +94,20 @@ dg_status make_tmap_out(CUtensorMap* m, void* base, long long N, long long M, lo
   return DG_OK;
 }
 
-template <int kW, int kH, class TO>
+template <int kW, class TO>
 dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
-  using S = Fp8Shape<kW, kH>;
+  using S = Fp8Shape<kW>;
   Fp8Maps maps;
   const int a_rows[3] = {16, 64, 128};
   for (int i = 0; i < 3; ++i) DG_TRY(make_tmap_codes(&maps.a[i], p.a, p.K, p.M, p.lda, a_rows[i]));
   for (int i = 0; i < 2; ++i) DG_TRY(make_tmap_codes(&maps.b[i], p.b, p.K, (long long)p.G * p.N, p.ldb, kW / (i ? 2 : 4)));
   memset(&maps.out, 0, sizeof maps.out);
   if (p.vec_out) DG_TRY(make_tmap_out<TO>(&maps.out, p.out, p.N, p.M, p.ldo));
-  const void* fn = (const void*)fp8_pair_kernel<kW, kH, TO>;
+  const void* fn = (const void*)fp8_pair_kernel<kW, TO>;
   DG_TRY(set_smem_attr(fn, S::kSmem, true));
   const long long tiles = p.off ? std::min(p.G, p.M) + (long long)p.M / 256 : ceil_div(p.M, 256);  // at most
-  const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, tiles * ceil_div(p.N, S::kBN));
-  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kW, kH, TO>, maps, p));
+  const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, tiles * ceil_div(p.N, kW));
+  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kW, TO>, maps, p));
   return DG_OK;
 }
 
@@ -116,9 +116,9 @@ dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
   if (p.M <= 16) return launch_small<TO>(p, st);
   const int pairs = device_sms() / 2;
   const long long tiles = p.off ? std::max<long long>(std::min(p.G, p.M), p.M / 256) : ceil_div(p.M, 256);
-  if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<128, 2, TO>(p, pairs, st);
-  if (tiles * ceil_div(p.N, 128) >= pairs / 2) return launch_pair<128, 1, TO>(p, pairs, st);
-  return launch_pair<64, 1, TO>(p, pairs, st);
+  if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<256, TO>(p, pairs, st);
+  if (tiles * ceil_div(p.N, 128) >= pairs / 2) return launch_pair<128, TO>(p, pairs, st);
+  return launch_pair<64, TO>(p, pairs, st);
 }
 
 dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, cudaStream_t st) {

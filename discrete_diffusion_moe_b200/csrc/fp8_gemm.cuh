@@ -9,16 +9,19 @@
 // accumulator element.  (With the weights as rows every column would need its
 // own scale from shared memory.)
 //
-// A unit is 256 rows x (kW * kH) columns of one group.  Per block of 128 k (one
-// stage: 128 bytes of each row, the width of the 128-byte swizzle) the leader
-// issues, for each of the kH column parts, four tcgen05.mma of M = 256, N = kW,
-// K = 32 into a fresh tensor-memory buffer; eight epilogue warps in each CTA
-// take the part's sums out, multiply them by the scales and add them in
-// registers, while the tensor cores work on the next parts in the other three
-// buffers.  fp32 throughout; one rounding at the store.  Parts of 128 columns
-// and four buffers, not 256 and two: a buffer goes around through the commit,
-// the epilogue and the release to the other CTA's leader, about 1000 cycles
-// beside its MMAs, which two buffers cannot hide.
+// A unit is 256 rows x kW columns of one group.  Per block of 128 k (one stage:
+// 128 bytes of each row, the width of the 128-byte swizzle) four tcgen05.mma of
+// M = 256, N = kW, K = 32 go into a fresh tensor-memory buffer; eight epilogue
+// warps in each CTA take the block's sums out, multiply them by the scales and
+// add them in registers, while the tensor cores work on the next block in
+// another buffer.  fp32 throughout; one rounding at the store.
+//
+// kW = 256 where there is enough work: shared memory is what bounds the kernel.
+// Per block a CTA's tensor cores read 16 KB of A and 128 bytes of each B row, and
+// 32 KB are written by the copies, at 128 bytes a cycle; with N = 128 A is read
+// twice, and the MMAs alone keep shared memory busy (measured: 950 cycles per
+// block of 256 columns, every barrier answering after 100 cycles or more, where
+// N = 256 leaves a third of it free).
 //
 // Each CTA of a pair copies its own 128 rows of A and half of the columns of B
 // (32 KB a stage at 256 columns), so a pair reads 512 rows per block.  Copies of
@@ -30,10 +33,10 @@
 // lines per instruction and took a sixth of a unit's time).
 //
 // Protocol of the barriers (rank 0 leads):
-//   full[s]         rank 0's: both CTAs' copies of a stage have landed
-//   acc_full[h][s]  both: part h's sums of the stage's block are in tensor
-//                   memory; those of all parts free the stage
-//   acc_empty[b]    rank 0's: the epilogue warps of both CTAs have read the buffer
+//   full[s]       rank 0's: both CTAs' copies of a stage have landed
+//   acc_full[s]   both: the sums of the stage's block are in tensor memory and the
+//                 stage is free
+//   acc_empty[b]  rank 0's: the epilogue warps of both CTAs have read the buffer
 //   sc_full, sc_empty[i]  each CTA's own: a slot of scales is written, is read
 // All waits are bounded; after one runs out the CTA stops working and stores
 // NaN for what it could not compute.
@@ -81,18 +84,6 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, 
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// Whether the phase of parity `parity` has completed, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 // Bounded wait without a result: when it runs out, *dead is set (then later waits
 // end at once) and the caller goes on; the kernel's results are marked at their
@@ -188,19 +179,17 @@ __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Table
   return j;
 }
 
-template <int kW, int kH>
+template <int kW>
 struct Fp8Shape {
-  static constexpr int kBN = kW * kH;
-  static constexpr int kBufs = 4;  // tensor-memory buffers of kW columns
-  static constexpr int kStages = kBN >= 256 ? 4 : (kBN >= 128 ? 5 : 6);
-  static constexpr int kStageA = 128 * 128, kPartB = (kW / 2) * 128, kStage = kStageA + kH * kPartB;
+  static constexpr int kBufs = kW >= 256 ? 2 : 4;  // tensor-memory buffers of kW columns
+  static constexpr int kStages = kW >= 256 ? 4 : (kW >= 128 ? 5 : 6);
+  static constexpr int kStageA = 128 * 128, kStageB = (kW / 2) * 128;
   static constexpr int kTurn = kFp8EpiWarps * 8192;  // two buffers of 32 rows x 128 bytes per warp
-  static constexpr int kCols = kH == 2 ? kW : kW / 2;  // columns of an epilogue warp
-  static constexpr int kReaders = kH == 2 ? kFp8EpiWarps / 2 : kFp8EpiWarps;  // warps of a CTA that read a buffer
-  // row and weight scales of four blocks per slot: [128][4] and [kH][4] floats
-  static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * kH;
-  static constexpr int kBars = kStages * (1 + kH) + kBufs + 2 * kScaleSlots + 1;
-  static constexpr int kSmem = 1024 + kStages * kStage + kTurn + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
+  static constexpr int kCols = kW / 2;               // columns of an epilogue warp
+  // row and weight scales of four blocks per slot: [4][128], and [4] for either half of the columns
+  static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * 2;
+  static constexpr int kBars = 2 * kStages + kBufs + 2 * kScaleSlots + 1;
+  static constexpr int kSmem = 1024 + kStages * (kStageA + kStageB) + kTurn + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
 };
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
@@ -218,17 +207,19 @@ __device__ __forceinline__ void bulk_wait_read() {
 // with the 128-byte swizzle (16-byte units by row): free of bank conflicts on
 // both sides.  With a tensor map the copy engine does the global side while the
 // warp goes on (columns from the matrix's end on are clipped); else the warp
-// stores whole rows itself: rows [0, rows), columns [0, cols).
+// stores whole rows itself: rows [0, rows), columns [0, cols).  `next`: the buffer
+// to use, the other one than the last pass's (of this unit or the one before).
 template <class TO, int kCols>
 __device__ __forceinline__ void store_turned(uint8_t* turn, const CUtensorMap* map, int x, int y, TO* out, long long ldo,
-                                             const float* acc, float w, int lane, int rows, int cols, bool vec) {
+                                             const float* acc, float w, int lane, int rows, int cols, bool vec, uint32_t& next) {
   constexpr int kPer = 128 / (int)sizeof(TO);  // columns per pass
   constexpr int kPass = kCols < kPer ? kCols : kPer;
   constexpr int kUnit = 16 / (int)sizeof(TO);  // columns per 16-byte unit
 #pragma unroll
   for (int c0 = 0; c0 < kCols; c0 += kPass) {
     if (c0 >= cols) break;
-    uint8_t* const buf = turn + ((c0 / kPass) & 1) * 4096;
+    uint8_t* const buf = turn + next;
+    next ^= 4096u;
     if (lane == 0) bulk_wait_read<1>();  // what this buffer held has been read
     __syncwarp();
 #pragma unroll
@@ -274,23 +265,23 @@ __device__ __forceinline__ void store_turned(uint8_t* turn, const CUtensorMap* m
   }
 }
 
-template <int kW, int kH, class TO>
+template <int kW, class TO>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8GemmParams p) {
-  using S = Fp8Shape<kW, kH>;
+  using S = Fp8Shape<kW>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Fp8Tables tabs;
   __shared__ int s_dead;
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const sA = smem;
   uint8_t* const sB = sA + S::kStages * S::kStageA;
-  uint8_t* const s_turn = sB + S::kStages * kH * S::kPartB;
+  uint8_t* const s_turn = sB + S::kStages * S::kStageB;
   float* const s_scale = (float*)(s_turn + S::kTurn);
   uint64_t* const bars = (uint64_t*)(s_scale + S::kScaleSlots * S::kScaleSlot);
   uint32_t* const tmem_slot = (uint32_t*)(bars + S::kBars);
   const uint32_t full = smem_u32(bars);
-  const uint32_t acc_full = full + 8 * S::kStages;            // [kH][kStages]
-  const uint32_t acc_empty = acc_full + 8 * kH * S::kStages;  // [kBufs]
+  const uint32_t acc_full = full + 8 * S::kStages;
+  const uint32_t acc_empty = acc_full + 8 * S::kStages;
   const uint32_t sc_full = acc_empty + 8 * S::kBufs;          // [kScaleSlots]
   const uint32_t sc_empty = sc_full + 8 * S::kScaleSlots;
   const uint32_t drain = sc_empty + 8 * S::kScaleSlots;
@@ -299,14 +290,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
-  const int n_tiles = (p.N + S::kBN - 1) / S::kBN;
+  const int n_tiles = (p.N + kW - 1) / kW;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full + 8 * s, 1);
-      for (int h = 0; h < kH; ++h) mbar_init(acc_full + 8 * (h * S::kStages + s), 1);
+      mbar_init(acc_full + 8 * s, 1);
     }
-    for (int b = 0; b < S::kBufs; ++b) mbar_init(acc_empty + 8 * b, 2 * S::kReaders);
+    for (int b = 0; b < S::kBufs; ++b) mbar_init(acc_empty + 8 * b, 2 * kFp8EpiWarps);
     for (int i = 0; i < S::kScaleSlots; ++i) {
       mbar_init(sc_full + 8 * i, 32);
       mbar_init(sc_empty + 8 * i, kFp8EpiWarps);
@@ -355,8 +346,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   const uint32_t tmem_base = *tmem_slot;
   if (p.off) m_tiles = tabs.first[p.G];
   const int U = m_tiles * n_tiles;
-  // columns of part h that the MMAs take: a multiple of 32; 0 for a part behind column N
-  auto part_cols = [&](const Fp8Job& j, int h) { return min(kW, max(0, p.N - j.n0 - h * kW + 31) & ~31); };
+  auto mma_cols = [&](const Fp8Job& j) { return min(kW, (p.N - j.n0 + 31) & ~31); };  // a multiple of 32
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RegsCopy));
@@ -369,29 +359,21 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       auto a_box = [&](int rows) { return rows <= 0 ? -1 : (rows <= 16 ? 0 : (rows <= 64 ? 1 : 2)); };
       auto a_bytes = [&](int box) { return box < 0 ? 0u : (box == 0 ? 16u : (box == 1 ? 64u : 128u)) * 128u; };
       for (int u = pair; u < U && !*dead; u += pairs) {
-        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
+        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
         const int mine = a_box(j.row1 - (j.row0 + (int)rank * 128));
         uint32_t tx = a_bytes(a_box(j.row1 - j.row0)) + a_bytes(a_box(j.row1 - j.row0 - 128));
-        int box[kH], yB[kH];
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const int n = part_cols(j, h);
-          box[h] = n == 0 ? -1 : (n <= kW / 2 ? 0 : 1);  // kW / 4 or kW / 2 rows from each CTA
-          yB[h] = j.group * p.N + j.n0 + h * kW + (int)rank * (n >> 1);
-          if (box[h] >= 0) tx += 2u * (uint32_t)(kW / (box[h] ? 2 : 4)) * 128u;
-        }
+        const int n = mma_cols(j);
+        const int box = n <= kW / 2 ? 0 : 1;  // kW / 4 or kW / 2 rows from each CTA
+        const int yB = j.group * p.N + j.n0 + (int)rank * (n >> 1);
+        tx += 2u * (uint32_t)(kW / (box ? 2 : 4)) * 128u;
         const int yA = j.row0 + (int)rank * 128;
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-#pragma unroll
-          for (int h = 0; h < kH; ++h) wait_or_die(acc_full + (h * S::kStages + s) * 8u, phase, dead);
+          wait_or_die(acc_full + s * 8u, phase, dead);
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s * 8u, tx);
             if (mine >= 0) tma_load_2d_pair(dstA + s * S::kStageA, &maps.a[mine], lead_bar + s * 8u, kb * 128, yA, pol_a);
-#pragma unroll
-            for (int h = 0; h < kH; ++h)
-              if (box[h] >= 0)
-                tma_load_2d_pair(dstB + (s * kH + h) * S::kPartB, &maps.b[box[h]], lead_bar + s * 8u, kb * 128, yB[h], pol_b);
+            tma_load_2d_pair(dstB + s * S::kStageB, &maps.b[box], lead_bar + s * 8u, kb * 128, yB, pol_b);
           }
           __syncwarp();
           ++issued;
@@ -409,44 +391,38 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     } else if (warp == 1 || warp == 3) {
       if (rank == 0) {
         // ---------------- MMAs (leader) ----------------
-        // Two warps take the parts (kH = 2) or the blocks (kH = 1) in turn: issuing a
-        // part's MMAs takes about as long as they run, and a ready barrier still
-        // answers after about 100 cycles, so one warp left the tensor cores idle
-        // half of the time (measured 1000 cycles per block of 512).
-        const int m = warp >> 1;
-        const int h = kH == 2 ? m : 0;
-        uint32_t s = kH == 2 ? 0 : m, phase = 0, b = m, b_phase = 1;
-        int skip = kH == 2 ? 0 : m;  // blocks until the next one of this warp
-        const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB)) + h * (S::kPartB / 16);
+        // Two warps take the blocks in turn: issuing a block's MMAs takes about as long
+        // as they run, so one warp would leave the tensor cores idle while it waits
+        // for the next block's barriers.
+        const uint32_t m = warp >> 1;
+        uint32_t s = m, phase = 0, b = m, b_phase = 1;
+        int kb = (int)m;  // block of this warp within the unit
+        const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
         for (int u = pair; u < U && !*dead; u += pairs) {
-          const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
-          const int n = part_cols(j, h);
-          const uint32_t idesc = idesc_e4m3_f32(256, n);
-          int kb = skip;
+          const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
+          const uint32_t idesc = idesc_e4m3_f32(256, mma_cols(j));
 #pragma unroll 1
-          for (; kb < p.KB; kb += 3 - kH) {
+          for (; kb < p.KB; kb += 2) {
             wait_or_die(full + s * 8u, phase, dead);
             wait_or_die(acc_empty + b * 8u, b_phase, dead);
             tc_fence_after();
             if (elect_one()) {
-              if (n > 0) {
-                const uint64_t da = descA + s * (S::kStageA / 16), db = descB + s * (kH * S::kPartB / 16);
+              const uint64_t da = descA + s * (S::kStageA / 16), db = descB + s * (S::kStageB / 16);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
-                  umma_e4m3_pair(tmem_base + b * kW, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-              }
-              umma_commit_pair_mc(acc_full + (h * S::kStages + s) * 8u, (uint16_t)3);
+              for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
+                umma_e4m3_pair(tmem_base + b * kW, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              umma_commit_pair_mc(acc_full + s * 8u, (uint16_t)3);
             }
             __syncwarp();
-            b ^= 2u;
-            if (b == (uint32_t)m) b_phase ^= 1;
-            s += 3 - kH;
+            b = (b + 2) % S::kBufs;
+            if (b == m) b_phase ^= 1;
+            s += 2;
             if (s >= S::kStages) {
               s -= S::kStages;
               phase ^= 1;
             }
           }
-          skip = kb - p.KB;
+          kb -= p.KB;
         }
         if (elect_one()) umma_commit_pair(drain);
         wait_or_die(drain, 0, dead);
@@ -457,9 +433,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // behind the copies of every stage, so it has to be issued early.
       uint32_t slot = 0, phase = 1;
       for (int u = pair; u < U && !*dead; u += pairs) {
-        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
+        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
         const int row = j.row0 + (int)rank * 128 + lane;
-        const int blk = min((j.n0 + min(lane >> 2, kH - 1) * kW) / kFp8Block, p.NB - 1);
+        const int blk = min((j.n0 + ((lane >> 2) & 1) * S::kCols) / kFp8Block, p.NB - 1);
         const float* const sb = p.sb + ((long long)j.group * p.NB + blk) * p.KB;
 #pragma unroll 1
         for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
@@ -470,13 +446,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[q][i] = row + 32 * i < j.row1 ? __ldg(src + row + 32 * i) : 0.f;
           }
-          if (lane < 4 * kH) vb = __ldg(sb + min(kb0 + (lane & 3), p.KB - 1));
+          if (lane < 8) vb = __ldg(sb + min(kb0 + (lane & 3), p.KB - 1));
           wait_or_die(sc_empty + slot * 8u, phase, dead);
           float* const dst = s_scale + slot * S::kScaleSlot;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4*>(dst)[32 * i + lane] = make_float4(v[0][i], v[1][i], v[2][i], v[3][i]);
-          if (lane < 4 * kH) dst[4 * 128 + lane] = vb;
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[q * 128 + 32 * i + lane] = v[q][i];
+          if (lane < 8) dst[4 * 128 + lane] = vb;
           mbar_arrive(sc_full + slot * 8u);
           if (++slot == S::kScaleSlots) {
             slot = 0;
@@ -487,83 +464,67 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     }
   } else {
     // ---------------- epilogue (both CTAs; warps 4..11) ----------------
-    // The two warps of a lane quarter take one part each (kH = 2), so that one adds
-    // while the other waits, or half of the only part's columns.  One wait, one
-    // arrival and one pair of scales per block: two warps per scheduler cannot
-    // hide more.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegsEpi));
     const int ew = warp - 4, quarter = warp & 3;  // tensor-memory lanes [32 quarter, +32)
-    const int h = kH == 2 ? ew >> 2 : 0;
-    const int c_first = kH == 2 ? 0 : (ew >> 2) * S::kCols;  // columns [c_first, +kCols) of part h
-    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(h * kW + c_first);
-    const uint32_t release_to = mapa_shared(acc_empty, 0) + (uint32_t)h * 8u;
-    const uint32_t my_full = acc_full + 8u * (uint32_t)(h * S::kStages);
-    uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0;
+    const int half = ew >> 2;                     // columns [half kCols, +kCols)
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * S::kCols);
+    const uint32_t release_to = mapa_shared(acc_empty, 0);
+    const float* const my_sa = s_scale + quarter * 32 + lane;
+    const float* const my_sb = s_scale + 4 * 128 + 4 * half;
+    uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0, turn_next = 0;
     for (int u = pair; u < U; u += pairs) {
-      const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, S::kBN);
+      const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
-      const int col = j.n0 + h * kW + c_first;
+      const int col = j.n0 + half * S::kCols;
       const bool work = row_w0 < j.row1 && col < p.N;
       float acc[S::kCols];
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
-      // scales of four blocks (sc4); those of the next four are read a block early
-      float4 sa4, sb4;
-      auto read_scales = [&]() {
-        wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-        const float4* const src = reinterpret_cast<const float4*>(s_scale + slot * S::kScaleSlot);
-        sa4 = src[quarter * 32 + lane];
-        sb4 = src[128 + h];
-      };
-      auto free_scales = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
-        if (++slot == S::kScaleSlots) {
-          slot = 0;
-          slot_phase ^= 1;
-        }
-      };
-      read_scales();
+      // the scales of the next block: read while this one is added (from the last
+      // block on the next slot is read, unused)
+      wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+      float sav = my_sa[slot * S::kScaleSlot], sbv = my_sb[slot * S::kScaleSlot];
       auto blocks = [&](auto works) {
-        float4 sc4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool ready = mbar_test_wait(my_full + s * 8u, s_phase);
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-          const int q = kb & 3;
-          if (q == 0) {
-            sc4 = make_float4(sa4.x * sb4.x, sa4.y * sb4.y, sa4.z * sb4.z, sa4.w * sb4.w);
-            free_scales();
-          }
-          const float sc = q < 2 ? (q == 0 ? sc4.x : sc4.y) : (q == 2 ? sc4.z : sc4.w);
-          if (!ready) wait_or_die(my_full + s * 8u, s_phase, dead);
-          __syncwarp();
+          const float sc = sav * sbv;
+          wait_or_die(acc_full + s * 8u, s_phase, dead);
           tc_fence_after();
           const uint32_t t0 = lane_base + b * kW;
           uint32_t r[32];
           if constexpr (decltype(works)::value) tmem_ld32_nowait(t0, r);
+          const int q1 = (kb + 1) & 3;
+          if (q1 == 0 || kb + 1 == p.KB) {  // this slot has been read
+            if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+            if (++slot == S::kScaleSlots) {
+              slot = 0;
+              slot_phase ^= 1;
+            }
+            if (kb + 1 < p.KB) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+          }
+          sav = my_sa[slot * S::kScaleSlot + q1 * 128];
+          sbv = my_sb[slot * S::kScaleSlot + q1];
           if (++s == S::kStages) {
             s = 0;
             s_phase ^= 1;
           }
-          // the next block's barrier is asked while this block is added (behind the
-          // last block it is the next unit's first)
-          ready = mbar_test_wait(my_full + s * 8u, s_phase);
           if constexpr (decltype(works)::value) {
-            tmem_wait32(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = fmaf(__uint_as_float(r[i]), sc, acc[i]);
-#pragma unroll
-            for (int c = 1; c < S::kCols / 32; ++c) {
-              tmem_ld32_nowait(t0 + c * 32, r);
+            for (int c = 0; c < S::kCols / 32; ++c) {
+              if (c > 0) tmem_ld32_nowait(t0 + c * 32, r);
               tmem_wait32(r);
+              if (c + 1 == S::kCols / 32) {  // all of the buffer is read: release it before adding
+                tc_fence_before();
+                if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
+              }
 #pragma unroll
               for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sc, acc[c * 32 + i]);
             }
+          } else {
+            tc_fence_before();
+            if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
           }
-          tc_fence_before();
-          if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
-          b = (b + kH) % S::kBufs;
-          if (q == 2 && kb + 2 < p.KB) read_scales();
+          b = (b + 1) % S::kBufs;
         }
       };
       // two loops: a condition inside the loop cost a register move per loaded value
@@ -578,7 +539,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       if (work)
         store_turned<TO, S::kCols>(s_turn + ew * 8192, whole ? &maps.out : nullptr, col, row_w0,
                                    static_cast<TO*>(p.out) + (long long)row_w0 * p.ldo + col, p.ldo, acc, w, lane, rows,
-                                   p.N - col, p.vec_out != 0);
+                                   p.N - col, p.vec_out != 0, turn_next);
     }
     if (lane == 0) bulk_wait_read<0>();
   }
