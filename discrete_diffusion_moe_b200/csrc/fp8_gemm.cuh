@@ -186,12 +186,19 @@ struct Fp8Shape {
   static constexpr int kStageA = 128 * 128, kStageB = (kW / 2) * 128;
   static constexpr int kTurn = kFp8EpiWarps * 8192;  // two buffers of 32 rows x 128 bytes per warp
   static constexpr int kCols = kW / 2;               // columns of an epilogue warp
-  // row and weight scales of four blocks per slot: [4][128], and [4] for either half of the columns
+  // row and weight scales of four blocks per slot: [128][4], and [4] for either half of the columns
   static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * 2;
   static constexpr int kBars = 2 * kStages + kBufs + 2 * kScaleSlots + 1;
   static constexpr int kSmem = 1024 + kStages * (kStageA + kStageB) + kTurn + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
 };
 
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// one arrival on `bar` when this thread's copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src), "r"(x),
                "r"(y)
@@ -429,38 +436,36 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       }
     } else if (warp == 2) {
       // ---------------- scales (both CTAs) ----------------
-      // Four blocks at a time, up to four slots ahead of the epilogue: a load queues
-      // behind the copies of every stage, so it has to be issued early.
+      // Asynchronous copies of four blocks' scales per slot, up to four slots ahead: a
+      // load queues behind the copies of every stage, and waiting for one slot before
+      // asking for the next set the pace of the whole kernel (950 cycles per block).
       uint32_t slot = 0, phase = 1;
       for (int u = pair; u < U && !*dead; u += pairs) {
         const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
-        const int row = j.row0 + (int)rank * 128 + lane;
+        const float* src[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) src[i] = p.sa + min(j.row0 + (int)rank * 128 + 32 * i + lane, j.row1 - 1);
         const int blk = min((j.n0 + ((lane >> 2) & 1) * S::kCols) / kFp8Block, p.NB - 1);
         const float* const sb = p.sb + ((long long)j.group * p.NB + blk) * p.KB;
 #pragma unroll 1
         for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
-          float v[4][4], vb = 0.f;
+          wait_or_die(sc_empty + slot * 8u, phase, dead);
+          const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float* const src = p.sa + (long long)min(kb0 + q, p.KB - 1) * p.lds;
+            const long long at = (long long)min(kb0 + q, p.KB - 1) * p.lds;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[q][i] = row + 32 * i < j.row1 ? __ldg(src + row + 32 * i) : 0.f;
+            for (int i = 0; i < 4; ++i) cp_async4(dst + (uint32_t)((32 * i + lane) * 4 + q) * 4u, src[i] + at);
           }
-          if (lane < 8) vb = __ldg(sb + min(kb0 + (lane & 3), p.KB - 1));
-          wait_or_die(sc_empty + slot * 8u, phase, dead);
-          float* const dst = s_scale + slot * S::kScaleSlot;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[q * 128 + 32 * i + lane] = v[q][i];
-          if (lane < 8) dst[4 * 128 + lane] = vb;
-          mbar_arrive(sc_full + slot * 8u);
+          if (lane < 8) cp_async4(dst + (uint32_t)(4 * 128 + lane) * 4u, sb + min(kb0 + (lane & 3), p.KB - 1));
+          cp_async_arrive(sc_full + slot * 8u);
           if (++slot == S::kScaleSlots) {
             slot = 0;
             phase ^= 1;
           }
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ---------------- epilogue (both CTAs; warps 4..11) ----------------
@@ -469,8 +474,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const int half = ew >> 2;                     // columns [half kCols, +kCols)
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * S::kCols);
     const uint32_t release_to = mapa_shared(acc_empty, 0);
-    const float* const my_sa = s_scale + quarter * 32 + lane;
-    const float* const my_sb = s_scale + 4 * 128 + 4 * half;
+    const float4* const my_sa = reinterpret_cast<const float4*>(s_scale) + quarter * 32 + lane;
+    const float4* const my_sb = reinterpret_cast<const float4*>(s_scale) + 128 + half;
     uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0, turn_next = 0;
     for (int u = pair; u < U; u += pairs) {
       const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
@@ -480,51 +485,59 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       float acc[S::kCols];
 #pragma unroll
       for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
-      // the scales of the next block: read while this one is added (from the last
-      // block on the next slot is read, unused)
-      wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-      float sav = my_sa[slot * S::kScaleSlot], sbv = my_sb[slot * S::kScaleSlot];
+      float4 sc4;  // the scales of four blocks
+      auto read_scales = [&]() {
+        wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+        const float4 a4 = my_sa[slot * (S::kScaleSlot / 4)], b4 = my_sb[slot * (S::kScaleSlot / 4)];
+        sc4 = make_float4(a4.x * b4.x, a4.y * b4.y, a4.z * b4.z, a4.w * b4.w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+        if (++slot == S::kScaleSlots) {
+          slot = 0;
+          slot_phase ^= 1;
+        }
+      };
+      read_scales();
       auto blocks = [&](auto works) {
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-          const float sc = sav * sbv;
+          const int q = kb & 3;
+          const float sc = q < 2 ? (q == 0 ? sc4.x : sc4.y) : (q == 2 ? sc4.z : sc4.w);
           wait_or_die(acc_full + s * 8u, s_phase, dead);
           tc_fence_after();
-          const uint32_t t0 = lane_base + b * kW;
-          uint32_t r[32];
-          if constexpr (decltype(works)::value) tmem_ld32_nowait(t0, r);
-          const int q1 = (kb + 1) & 3;
-          if (q1 == 0 || kb + 1 == p.KB) {  // this slot has been read
-            if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
-            if (++slot == S::kScaleSlots) {
-              slot = 0;
-              slot_phase ^= 1;
-            }
-            if (kb + 1 < p.KB) wait_or_die(sc_full + slot * 8u, slot_phase, dead);
-          }
-          sav = my_sa[slot * S::kScaleSlot + q1 * 128];
-          sbv = my_sb[slot * S::kScaleSlot + q1];
-          if (++s == S::kStages) {
-            s = 0;
-            s_phase ^= 1;
-          }
+          // Two loads at a time, and the buffer is released before the last sums are
+          // added: what lies between the barrier and the release is on the path
+          // MMA - commit - epilogue - release - MMA that bounds the kernel.
           if constexpr (decltype(works)::value) {
+            const uint32_t t0 = lane_base + b * kW;
+            constexpr int kLd = S::kCols / 32, kTwo = kLd < 2 ? kLd : 2;
+            uint32_t r[kTwo][32];
 #pragma unroll
-            for (int c = 0; c < S::kCols / 32; ++c) {
-              if (c > 0) tmem_ld32_nowait(t0 + c * 32, r);
-              tmem_wait32(r);
-              if (c + 1 == S::kCols / 32) {  // all of the buffer is read: release it before adding
+            for (int c0 = 0; c0 < kLd; c0 += kTwo) {
+#pragma unroll
+              for (int c = 0; c < kTwo; ++c) tmem_ld32_nowait(t0 + (c0 + c) * 32, r[c]);
+#pragma unroll
+              for (int c = 0; c < kTwo; ++c) tmem_wait32(r[c]);
+              if (c0 + kTwo == kLd) {
                 tc_fence_before();
                 if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
               }
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sc, acc[c * 32 + i]);
+              for (int c = 0; c < kTwo; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  acc[(c0 + c) * 32 + i] = fmaf(__uint_as_float(r[c][i]), sc, acc[(c0 + c) * 32 + i]);
             }
           } else {
             tc_fence_before();
             if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
           }
           b = (b + 1) % S::kBufs;
+          if (++s == S::kStages) {
+            s = 0;
+            s_phase ^= 1;
+          }
+          if (q == 3 && kb + 1 < p.KB) read_scales();
         }
       };
       // two loops: a condition inside the loop cost a register move per loaded value
