@@ -10,8 +10,6 @@ current one; work goes to `stream` (the device's current stream by default).
 Wrong shapes, types or strides raise ValueError, what the library itself
 refuses raises DgError; nothing is launched then."""
 
-import ctypes
-
 import torch
 
 from . import DG_ACT_NONE, DG_ACT_SWIGLU, DG_ACT_SWIGLU_INTERLEAVED, DG_BF16, DG_F16, DG_F32, check, lib
@@ -21,34 +19,31 @@ _ACT = {None: DG_ACT_NONE, "swiglu": DG_ACT_SWIGLU, "swiglu_interleaved": DG_ACT
 _E4M3 = torch.float8_e4m3fn
 
 
-def _require(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _fail(what):
+    raise ValueError(what)
 
 
 def _blocks(n):
-    return (n + 127) // 128
+    return (n + 127) >> 7
 
 
-def _pitch(t, least):
-    """Elements between rows of a 2-D tensor (any value will do for one row)."""
-    return t.stride(0) if t.shape[0] > 1 else least
-
-
-def _on(device, *tensors):
-    for t in tensors:
-        _require(t is None or t.device == device, "tensors on different devices")
-
-
-def _launch(fn, device, stream, *args):
-    """One library call on `device` and `stream`."""
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    _require(s.device == device, "the stream is on another device than the tensors")
-    if torch.cuda.current_device() == device.index:
-        check(fn(*args, s.cuda_stream))
+def _launch(fn, device, stream, args):
+    """One library call on `device` and `stream` (its current one for None).
+    These calls take a few microseconds on the GPU, so the host side keeps to
+    plain integers: the raw stream and the current device's number."""
+    index = device.index
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream.device == device or _fail("the stream is on another device than the tensors")
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            check(fn(*args, s.cuda_stream))
+            status = fn(*args, raw)
+    if status:
+        check(status)
 
 
 def _empty(shape, dtype, device, stream):
@@ -61,20 +56,35 @@ def _empty(shape, dtype, device, stream):
 
 def _new_codes(shape, device, stream):
     K = shape[-1]
-    pitch = (K + 15) // 16 * 16
-    q = _empty((*shape[:-1], pitch), _E4M3, device, stream)
-    return q if pitch == K else q[..., :K]
+    if K & 15 == 0:
+        return _empty(shape, _E4M3, device, stream)
+    return _empty((*shape[:-1], (K + 15) & ~15), _E4M3, device, stream)[..., :K]
 
 
 def _check_codes(name, t, dim):
-    _require(t.dtype == _E4M3 and t.is_cuda and t.dim() == dim, f"{name}: a {dim}-D float8_e4m3fn CUDA tensor is needed")
-    _require(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{name}: the columns must be contiguous")
+    if t.dtype is not _E4M3 or not t.is_cuda or t.dim() != dim:
+        _fail(f"{name}: a {dim}-D float8_e4m3fn CUDA tensor is needed")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        _fail(f"{name}: the columns must be contiguous")
 
 
-def _check_row_scale(name, s, rows, K):
-    _require(s.dtype == torch.float32 and s.dim() == 2 and tuple(s.shape) == (_blocks(K), rows),
-             f"{name}: float32 [{_blocks(K)}, {rows}] is needed, got {s.dtype} {list(s.shape)}")
-    _require(rows <= 1 or s.stride(1) == 1, f"{name}: each block's row scales must be contiguous")
+def _row_scale_pitch(name, s, device, rows, blocks):
+    """Elements between the blocks of a [blocks, rows] tensor of row scales."""
+    if s.dtype is not torch.float32 or s.shape != (blocks, rows):
+        _fail(f"{name}: float32 [{blocks}, {rows}] is needed, got {s.dtype} {list(s.shape)}")
+    if s.device != device:
+        _fail("tensors on different devices")
+    pitch, inner = s.stride()
+    if inner != 1 and rows > 1:
+        _fail(f"{name}: each block's row scales must be contiguous")
+    return pitch if blocks > 1 else rows
+
+
+def _check_vector(name, t, device, dtype, n):
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        _fail(f"{name}: contiguous {dtype} [{n}] is needed")
+    if t.device != device:
+        _fail("tensors on different devices")
 
 
 def fp8_quantize(x, index=None, act=None, out=None, stream=None):
@@ -83,102 +93,125 @@ def fp8_quantize(x, index=None, act=None, out=None, stream=None):
     (codes [rows, K], scale [ceil(K / 128), rows]).  index (int32 [rows]):
     output row r takes row index[r] of x; indices outside x read as zeros.
     out: an earlier result to write into."""
-    _require(x.is_cuda and x.dim() == 2 and x.dtype in _DTYPE, "x: a 2-D bf16, fp16 or fp32 CUDA tensor is needed")
-    _require(act in _ACT, f"act: None, 'swiglu' or 'swiglu_interleaved', got {act!r}")
-    _require(x.shape[1] <= 1 or x.stride(1) == 1, "x: the columns must be contiguous")
-    K = x.shape[1]
-    if act is not None:
-        _require(K % 2 == 0, "x: an even number of columns is needed for SwiGLU")
-        K //= 2
-    _require(K >= 1, "x: at least one column is needed")
-    rows = x.shape[0]
+    dtype = _DTYPE.get(x.dtype)
+    if dtype is None or not x.is_cuda or x.dim() != 2:
+        _fail("x: a 2-D bf16, fp16 or fp32 CUDA tensor is needed")
+    if act not in _ACT:
+        _fail(f"act: None, 'swiglu' or 'swiglu_interleaved', got {act!r}")
+    device = x.device
+    x_rows, cols = x.shape
+    ldx, inner = x.stride()
+    if inner != 1 and cols > 1:
+        _fail("x: the columns must be contiguous")
+    if cols < 1 or (act is not None and cols & 1):
+        _fail("x: at least one column, and an even number of them for SwiGLU, is needed")
+    K = cols if act is None else cols >> 1
+    rows, index_ptr = x_rows, None
     if index is not None:
-        _require(index.dtype == torch.int32 and index.dim() == 1 and index.is_contiguous(),
-                 "index: a contiguous 1-D int32 tensor is needed")
+        if index.dim() != 1:
+            _fail("index: a 1-D tensor is needed")
         rows = index.shape[0]
+        _check_vector("index", index, device, torch.int32, rows)
+        index_ptr = index.data_ptr()
+    KB = (K + 127) >> 7
     if out is None:
-        q, scale = _new_codes((rows, K), x.device, stream), _empty((_blocks(K), rows), torch.float32, x.device, stream)
+        q, scale, lds = _new_codes((rows, K), device, stream), _empty((KB, rows), torch.float32, device, stream), rows
     else:
         q, scale = out
         _check_codes("out[0]", q, 2)
-        _require(tuple(q.shape) == (rows, K), f"out[0]: [{rows}, {K}] is needed")
-        _check_row_scale("out[1]", scale, rows, K)
-    _on(x.device, index, q, scale)
-    _launch(lib.dg_fp8_quantize, x.device, stream, x.data_ptr(), _DTYPE[x.dtype], _pitch(x, x.shape[1]), x.shape[0],
-            index.data_ptr() if index is not None else None, _ACT[act], rows, K, q.data_ptr(),
-            _pitch(q, (K + 15) // 16 * 16), scale.data_ptr(), max(scale.stride(0), rows))
+        if q.shape != (rows, K) or q.device != device:
+            _fail(f"out[0]: [{rows}, {K}] on x's device is needed")
+        lds = _row_scale_pitch("out[1]", scale, device, rows, KB)
+    _launch(lib.dg_fp8_quantize, device, stream,
+            (x.data_ptr(), dtype, ldx if x_rows > 1 else cols, x_rows, index_ptr, _ACT[act], rows, K, q.data_ptr(),
+             q.stride(0) if rows > 1 else (K + 15) & ~15, scale.data_ptr(), lds))
     return q, scale
 
 
 def _weight_pitch(name, t):
-    """Elements between the rows of a [N, K] or [G, N, K] tensor."""
-    G, N, K = t.shape if t.dim() == 3 else (1, *t.shape)
-    _require(K <= 1 or t.stride(-1) == 1, f"{name}: the columns must be contiguous")
-    if N > 1:
-        pitch = t.stride(-2)
-        _require(G <= 1 or t.stride(0) == N * pitch, f"{name}: the matrices must follow one another")
-        return pitch
-    return t.stride(0) if G > 1 else None
+    """Elements between the rows of a [N, K] or [G, N, K] tensor (None: any)."""
+    if t.dim() == 2:
+        return t.stride(0) if t.shape[0] > 1 else None
+    G, N = t.shape[:2]
+    if N == 1:
+        return t.stride(0) if G > 1 else None
+    pitch = t.stride(1)
+    if G > 1 and t.stride(0) != N * pitch:
+        _fail(f"{name}: the matrices must follow one another")
+    return pitch
 
 
 def fp8_quantize_blocks(w, out=None, stream=None):
     """Quantise weights w [N, K] or [G, N, K] (bf16, fp16 or fp32) to (codes of
     the same shape, scale [(G,) ceil(N / 128), ceil(K / 128)])."""
-    _require(w.is_cuda and w.dim() in (2, 3) and w.dtype in _DTYPE,
-             "w: a 2-D or 3-D bf16, fp16 or fp32 CUDA tensor is needed")
+    dtype = _DTYPE.get(w.dtype)
+    if dtype is None or not w.is_cuda or w.dim() not in (2, 3):
+        _fail("w: a 2-D or 3-D bf16, fp16 or fp32 CUDA tensor is needed")
     G, N, K = w.shape if w.dim() == 3 else (1, *w.shape)
-    _require(N >= 1 and K >= 1, "w: at least one row and one column are needed")
+    if N < 1 or K < 1:
+        _fail("w: at least one row and one column are needed")
+    if w.stride(-1) != 1 and K > 1:
+        _fail("w: the columns must be contiguous")
     shape = (*w.shape[:-2], _blocks(N), _blocks(K))
     if out is None:
         q, scale = _new_codes(tuple(w.shape), w.device, stream), _empty(shape, torch.float32, w.device, stream)
     else:
         q, scale = out
         _check_codes("out[0]", q, w.dim())
-        _require(q.shape == w.shape, "out[0]: the shape of w is needed")
-        _require(scale.dtype == torch.float32 and tuple(scale.shape) == shape and scale.is_contiguous(),
-                 f"out[1]: contiguous float32 {list(shape)} is needed")
-    _on(w.device, q, scale)
+        if q.shape != w.shape or q.device != w.device:
+            _fail("out[0]: the shape and device of w are needed")
+        if scale.dtype != torch.float32 or scale.shape != shape or not scale.is_contiguous() or scale.device != w.device:
+            _fail(f"out[1]: contiguous float32 {list(shape)} on w's device is needed")
     ldw, ldq = _weight_pitch("w", w), _weight_pitch("out[0]", q)
-    _launch(lib.dg_fp8_quantize_blocks, w.device, stream, w.data_ptr(), _DTYPE[w.dtype], K if ldw is None else ldw, G, N,
-            K, q.data_ptr(), (K + 15) // 16 * 16 if ldq is None else ldq, scale.data_ptr())
+    _launch(lib.dg_fp8_quantize_blocks, w.device, stream,
+            (w.data_ptr(), dtype, K if ldw is None else ldw, G, N, K, q.data_ptr(),
+             (K + 15) & ~15 if ldq is None else ldq, scale.data_ptr()))
     return q, scale
 
 
 def _product(a, a_scale, b, b_scale, off, row_weight, out_dtype, out, stream):
-    grouped = off is not None
     _check_codes("a", a, 2)
-    _check_codes("b", b, 3 if grouped else 2)
+    _check_codes("b", b, 2 if off is None else 3)
+    device = a.device
     M, K = a.shape
-    N = b.shape[-2]
-    G = b.shape[0] if grouped else 1
-    _require(b.shape[-1] == K, f"a has {K} columns, b {b.shape[-1]}")
-    _check_row_scale("a_scale", a_scale, M, K)
-    shape = (G, _blocks(N), _blocks(K)) if grouped else (_blocks(N), _blocks(K))
-    _require(b_scale.dtype == torch.float32 and tuple(b_scale.shape) == shape and b_scale.is_contiguous(),
-             f"b_scale: contiguous float32 {list(shape)} is needed")
-    if grouped:
-        _require(off.dtype == torch.int32 and off.dim() == 1 and off.shape[0] == G + 1 and off.is_contiguous(),
-                 f"off: contiguous int32 [{G + 1}] is needed")
+    KB, k16 = (K + 127) >> 7, (K + 15) & ~15
+    N, k_b = b.shape[-2:]
+    if k_b != K:
+        _fail(f"a has {K} columns, b {k_b}")
+    lds = _row_scale_pitch("a_scale", a_scale, device, M, KB)
+    shape = ((N + 127) >> 7, KB) if off is None else (b.shape[0], (N + 127) >> 7, KB)
+    if b_scale.dtype is not torch.float32 or b_scale.shape != shape or not b_scale.is_contiguous():
+        _fail(f"b_scale: contiguous float32 {list(shape)} is needed")
+    if b.device != device or b_scale.device != device:
+        _fail("tensors on different devices")
+    weight_ptr = None
     if row_weight is not None:
-        _require(row_weight.dtype == torch.float32 and tuple(row_weight.shape) == (M,) and row_weight.is_contiguous(),
-                 f"row_weight: contiguous float32 [{M}] is needed")
+        _check_vector("row_weight", row_weight, device, torch.float32, M)
+        weight_ptr = row_weight.data_ptr()
     if out is None:
-        _require(out_dtype in _DTYPE, f"out_dtype: bf16, fp16 or fp32, got {out_dtype}")
-        out = _empty((M, N), out_dtype, a.device, stream)
+        dtype = _DTYPE.get(out_dtype)
+        if dtype is None:
+            _fail(f"out_dtype: bf16, fp16 or fp32, got {out_dtype}")
+        out, ldo = _empty((M, N), out_dtype, device, stream), N
     else:
-        _require(out.dtype in _DTYPE and tuple(out.shape) == (M, N) and (N <= 1 or out.stride(1) == 1),
-                 f"out: bf16, fp16 or fp32 [{M}, {N}] with contiguous columns is needed")
-    _on(a.device, a_scale, b, b_scale, off, row_weight, out)
-    k16 = (K + 15) // 16 * 16
+        dtype = _DTYPE.get(out.dtype)
+        if dtype is None or out.shape != (M, N) or out.device != device or (out.stride(1) != 1 and N > 1):
+            _fail(f"out: bf16, fp16 or fp32 [{M}, {N}] with contiguous columns on a's device is needed")
+        ldo = out.stride(0) if M > 1 else N
     ldb = _weight_pitch("b", b)
-    head = (a.data_ptr(), _pitch(a, k16), a_scale.data_ptr(), max(a_scale.stride(0), M), b.data_ptr(),
-            k16 if ldb is None else ldb, b_scale.data_ptr())
-    tail = (M, N, K, row_weight.data_ptr() if row_weight is not None else None, out.data_ptr(), _DTYPE[out.dtype],
-            _pitch(out, N))
-    if grouped:
-        _launch(lib.dg_fp8_grouped_gemm, a.device, stream, *head, off.data_ptr(), G, *tail)
+    lda = a.stride(0) if M > 1 else k16
+    if ldb is None:
+        ldb = k16
+    if off is None:
+        _launch(lib.dg_fp8_gemm, device, stream,
+                (a.data_ptr(), lda, a_scale.data_ptr(), lds, b.data_ptr(), ldb, b_scale.data_ptr(), M, N, K, weight_ptr,
+                 out.data_ptr(), dtype, ldo))
     else:
-        _launch(lib.dg_fp8_gemm, a.device, stream, *head, *tail)
+        G = shape[0]
+        _check_vector("off", off, device, torch.int32, G + 1)
+        _launch(lib.dg_fp8_grouped_gemm, device, stream,
+                (a.data_ptr(), lda, a_scale.data_ptr(), lds, b.data_ptr(), ldb, b_scale.data_ptr(), off.data_ptr(), G, M, N,
+                 K, weight_ptr, out.data_ptr(), dtype, ldo))
     return out
 
 
@@ -195,5 +228,5 @@ def fp8_grouped_gemm(a, a_scale, b, b_scale, off, row_weight=None, out_dtype=tor
     [off[g], off[g + 1]) take matrix g (off: int32 [G + 1], non-decreasing).
     Rows outside [off[0], off[G]) are not written: they keep what `out` holds,
     and are undefined when `out` is not given."""
-    _require(off is not None, "off is needed")
+    off is not None or _fail("off is needed")
     return _product(a, a_scale, b, b_scale, off, row_weight, out_dtype, out, stream)
