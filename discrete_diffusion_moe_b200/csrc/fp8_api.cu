@@ -9,10 +9,14 @@
 #include "fp8_gemm.cuh"
 #include "fp8_quant.cuh"
 #include "fp8_small.cuh"
+#include "fp8_stream.cuh"
 #include "host.cuh"
 
 using namespace dg;
 
+#ifndef FP8_STREAM_ROWS
+#define FP8_STREAM_ROWS 64
+#endif
 namespace {
 
 constexpr long long kMaxDim = 2147483647ll;
@@ -111,11 +115,27 @@ dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
   return DG_OK;
 }
 
+template <int kTok, class TO>
+dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
+  using S = Fp8StreamShape<kTok>;
+  Fp8StreamMaps maps;
+  const int rows[3] = {16, 32, kTok};
+  DG_TRY(make_tmap_codes(&maps.w, p.b, p.K, (long long)p.G * p.N, p.ldb, 128));
+  for (int i = 0; i < 3; ++i) DG_TRY(make_tmap_codes(&maps.t[i], p.a, p.K, p.M, p.lda, rows[i]));
+  DG_TRY(set_smem_attr((const void*)fp8_stream_kernel<kTok, TO>, S::kSmem, true));
+  const long long chunks = p.off ? std::min(p.G, p.M) + (long long)p.M / kTok : ceil_div(p.M, kTok);  // at most
+  const unsigned grid = (unsigned)std::min<long long>(sms, chunks * ceil_div(p.N, 128));
+  DG_CUDA(Launch(dim3(grid), dim3(kStreamThreads), S::kSmem, st)(fp8_stream_kernel<kTok, TO>, maps, p));
+  return DG_OK;
+}
+
 template <class TO>
 dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
   if (p.M <= 16) return launch_small<TO>(p, st);
-  const int pairs = device_sms() / 2;
-  const long long tiles = p.off ? std::max<long long>(std::min(p.G, p.M), p.M / 256) : ceil_div(p.M, 256);
+  const int sms = device_sms(), pairs = sms / 2;
+  const long long groups = p.off ? std::min(p.G, p.M) : 1;  // that may have rows
+  if (p.M <= FP8_STREAM_ROWS * groups && groups * ceil_div(p.N, 128) >= sms) return launch_stream<64, TO>(p, sms, st);
+  const long long tiles = p.off ? std::max<long long>(groups, p.M / 256) : ceil_div(p.M, 256);
   if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<256, TO>(p, pairs, st);
   if (tiles * ceil_div(p.N, 128) >= pairs / 2) return launch_pair<128, TO>(p, pairs, st);
   return launch_pair<64, TO>(p, pairs, st);

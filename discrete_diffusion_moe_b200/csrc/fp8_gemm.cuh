@@ -85,17 +85,30 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Bounded wait without a result: when it runs out, *dead is set (then later waits
-// end at once) and the caller goes on; the kernel's results are marked at their
-// store.  Warps are converged again after it.
-__device__ __forceinline__ void wait_or_die(uint32_t bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ int ld_shared_flag(uint32_t addr) {
+  int v;
+  asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Bounded wait of a whole warp without a result: when it runs out, the flag at
+// shared address `dead` is set (then later waits end at once) and the caller goes
+// on; the kernel's results are marked at their store.
+__device__ __forceinline__ void wait_or_die(uint32_t bar, uint32_t parity, uint32_t dead) {
   if (!mbar_try_wait(bar, parity)) {
     const unsigned long long t0 = globaltimer_ns();
     uint32_t n = 0;
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity)) {
-      if ((++n & 255u) == 0u && (*dead || globaltimer_ns() - t0 > kWaitLimitNs)) {
-        *dead = 1;
+      if ((++n & 255u) == 0u && (ld_shared_flag(dead) || globaltimer_ns() - t0 > kWaitLimitNs)) {
+        asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
         break;
       }
     }
@@ -143,23 +156,52 @@ struct Fp8Maps {
 };
 
 struct Fp8Tables {
-  int first[kFp8MaxGroups + 1];  // 256-row tiles of the groups before g
+  int first[kFp8MaxGroups + 1];  // row tiles of the groups before g
   int row0[kFp8MaxGroups];
   int row1[kFp8MaxGroups];
 };
 
+// The groups' rows and their prefix sums of tiles of kRows rows (one warp).
+template <int kRows>
+__device__ __forceinline__ void fp8_tables(const Fp8GemmParams& p, Fp8Tables* tb, int lane) {
+  int sum = 0;
+  for (int base = 0; base < p.G; base += 32) {
+    const int g = base + lane;
+    RowRange r{0, 0};
+    if (g < p.G) r = group_rows(p.off, g, p.M);
+    const int t = (r.row1 - r.row0 + kRows - 1) / kRows;
+    int inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (g < p.G) {
+      tb->first[g] = sum + inc - t;
+      tb->row0[g] = r.row0;
+      tb->row1[g] = r.row1;
+    }
+    sum += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) tb->first[p.G] = sum;
+}
+
 struct Fp8Job {
-  int group, row0, row1, n0;  // the unit's rows [row0, row1) of at most 256, first column
+  int group, row0, row1, n0;  // the unit's rows [row0, row1) of at most kRows, first column of B
 };
 
+// Unit u of tiles of kRows rows x bn columns: n_tiles column tiles, m_tiles row
+// tiles (all groups together); a group's row tiles of one column tile are
+// consecutive units, which share their columns of B.
+template <int kRows>
 __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Tables* tb, int u, int m_tiles, int n_tiles,
                                           int bn) {
   Fp8Job j;
   if (!p.off) {
-    const int nt = u / m_tiles, mt = u - nt * m_tiles;  // consecutive units share their columns of B
+    const int nt = u / m_tiles, mt = u - nt * m_tiles;
     j.group = 0;
-    j.row0 = mt * 256;
-    j.row1 = min(p.M, j.row0 + 256);
+    j.row0 = mt * kRows;
+    j.row1 = min(p.M, j.row0 + kRows);
     j.n0 = nt * bn;
     return j;
   }
@@ -173,8 +215,8 @@ __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Table
   const int r = u - tb->first[lo] * n_tiles;
   const int nt = r / tiles, mt = r - nt * tiles;
   j.group = lo;
-  j.row0 = tb->row0[lo] + mt * 256;
-  j.row1 = min(tb->row1[lo], j.row0 + 256);
+  j.row0 = tb->row0[lo] + mt * kRows;
+  j.row1 = min(tb->row1[lo], j.row0 + kRows);
   j.n0 = nt * bn;
   return j;
 }
@@ -292,7 +334,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   const uint32_t sc_full = acc_empty + 8 * S::kBufs;          // [kScaleSlots]
   const uint32_t sc_empty = sc_full + 8 * S::kScaleSlots;
   const uint32_t drain = sc_empty + 8 * S::kScaleSlots;
-  volatile int* const dead = &s_dead;
+  const uint32_t dead = smem_u32(&s_dead);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -319,28 +361,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   grid_dep_wait();
   grid_dep_launch();
   int m_tiles = (p.M + 255) / 256;
-  if (p.off && warp == 4) {
-    int sum = 0;
-    for (int base = 0; base < p.G; base += 32) {
-      const int g = base + lane;
-      RowRange r{0, 0};
-      if (g < p.G) r = group_rows(p.off, g, p.M);
-      const int t = (r.row1 - r.row0 + 255) / 256;
-      int inc = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (g < p.G) {
-        tabs.first[g] = sum + inc - t;
-        tabs.row0[g] = r.row0;
-        tabs.row1[g] = r.row1;
-      }
-      sum += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) tabs.first[p.G] = sum;
-  }
+  if (p.off && warp == 4) fp8_tables<256>(p, &tabs, lane);
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers initialised before either signals one
   if (warp == 1) {
@@ -365,8 +386,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
       auto a_box = [&](int rows) { return rows <= 0 ? -1 : (rows <= 16 ? 0 : (rows <= 64 ? 1 : 2)); };
       auto a_bytes = [&](int box) { return box < 0 ? 0u : (box == 0 ? 16u : (box == 1 ? 64u : 128u)) * 128u; };
-      for (int u = pair; u < U && !*dead; u += pairs) {
-        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
+      for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
+        const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
         const int mine = a_box(j.row1 - (j.row0 + (int)rank * 128));
         uint32_t tx = a_bytes(a_box(j.row1 - j.row0)) + a_bytes(a_box(j.row1 - j.row0 - 128));
         const int n = mma_cols(j);
@@ -405,8 +426,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         uint32_t s = m, phase = 0, b = m, b_phase = 1;
         int kb = (int)m;  // block of this warp within the unit
         const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
-        for (int u = pair; u < U && !*dead; u += pairs) {
-          const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
+        for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
+          const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
           const uint32_t idesc = idesc_e4m3_f32(256, mma_cols(j));
 #pragma unroll 1
           for (; kb < p.KB; kb += 2) {
@@ -440,8 +461,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // load queues behind the copies of every stage, and waiting for one slot before
       // asking for the next set the pace of the whole kernel (950 cycles per block).
       uint32_t slot = 0, phase = 1;
-      for (int u = pair; u < U && !*dead; u += pairs) {
-        const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
+      for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
+        const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
         const float* src[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) src[i] = p.sa + min(j.row0 + (int)rank * 128 + 32 * i + lane, j.row1 - 1);
@@ -478,7 +499,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const float4* const my_sb = reinterpret_cast<const float4*>(s_scale) + 128 + half;
     uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0, turn_next = 0;
     for (int u = pair; u < U; u += pairs) {
-      const Fp8Job j = fp8_job(p, &tabs, u, m_tiles, n_tiles, kW);
+      const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
       const int col = j.n0 + half * S::kCols;
       const bool work = row_w0 < j.row1 && col < p.N;
@@ -545,7 +566,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       else      blocks(std::false_type{});
       const int row = row_w0 + lane;
       // a wait that ran out: what was added is not the product
-      const float w = *dead ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
+      const float w = ld_shared_flag(dead) ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
       // the copy engine clips at the matrix's edges only, not at a group's last row
       const int rows = min(32, j.row1 - row_w0);
       const bool whole = S::kCols * sizeof(TO) >= 128 && p.vec_out && (rows == 32 || !p.off);

@@ -10,8 +10,8 @@
 // side: a tcgen05 tile would spend 128 rows on one token, and here the weights
 // go from global memory to registers without a stop in shared memory.  The
 // order of k inside a block is free as long as A and B agree, so lane (g, t)
-// of a warp takes the 32 consecutive bytes [32 t, 32 t + 32) of its rows: two
-// 16-byte loads per row, four products per block.  The eight warps of a CTA
+// of a warp takes bytes [16 t, 16 t + 16) of both halves of its rows' 128: two
+// 16-byte loads per row, each of whole sectors, and four products per block.  The eight warps of a CTA
 // share its features and take every eighth block of K each: all of a CTA's
 // loads are in flight together.  Their fp32 partial sums meet in shared memory
 // in the order of the warps (the result does not depend on timing).
@@ -26,9 +26,12 @@ namespace dg {
 struct RowRange {
   int row0, row1;
 };
+__device__ __forceinline__ RowRange held_inside(int off0, int off1, int M) {
+  const int r0 = min(max(off0, 0), M);
+  return {r0, min(max(off1, r0), M)};
+}
 __device__ __forceinline__ RowRange group_rows(const int32_t* off, int g, int M) {
-  const int r0 = min(max(__ldg(off + g), 0), M);
-  return {r0, min(max(__ldg(off + g + 1), r0), M)};
+  return held_inside(__ldg(off + g), __ldg(off + g + 1), M);
 }
 
 struct Fp8GemmParams {
@@ -68,17 +71,17 @@ __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
 __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int n) {
   return n >= 4 ? w : (n <= 0 ? 0u : (w & ((1u << (8 * n)) - 1u)));
 }
-// 32 consecutive codes of one row from column k0 on; columns from K on read as 0.
-// A 16-byte word is read only where its first byte is inside the row, so the
-// reads stay within the row's 16-byte pitch.
+// A lane's 32 codes of one row's block: 16 from column k0 on and 16 from k0 + 64
+// on; columns from K on read as 0.  A 16-byte word is read only where its first
+// byte is inside the row, so the reads stay within the row's 16-byte pitch.
 template <bool kStream>
 __device__ __forceinline__ void load_codes32(uint32_t (&w)[8], const uint8_t* row, int k0, int K, bool on) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (on && k0 + 16 * h < K) {
-      if constexpr (kStream) v = ld_stream(row + k0 + 16 * h);
-      else v = __ldg(reinterpret_cast<const uint4*>(row + k0 + 16 * h));
+    if (on && k0 + 64 * h < K) {
+      if constexpr (kStream) v = ld_stream(row + k0 + 64 * h);
+      else v = __ldg(reinterpret_cast<const uint4*>(row + k0 + 64 * h));
     }
     w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
   }
@@ -97,24 +100,50 @@ __global__ void __launch_bounds__(32 * kSmallWarps) fp8_small_kernel(const Fp8Ge
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kFeat;
 
-  // the blockIdx.y-th group that has rows
+  // The blockIdx.y-th group that has rows: each lane looks at eight groups, their
+  // offsets loaded together (one latency before the weights can be asked for).
   int grp = 0, row0 = 0, row1 = p.M;
   if (p.off) {
     int want = (int)blockIdx.y;
     grp = -1;
-    for (int base = 0; base < p.G; base += 32) {
-      RowRange r{0, 0};
-      if (base + lane < p.G) r = group_rows(p.off, base + lane, p.M);
-      const unsigned has = __ballot_sync(0xffffffffu, r.row1 > r.row0);
-      if (want < __popc(has)) {
-        const bool mine = r.row1 > r.row0 && __popc(has & ((1u << lane) - 1u)) == want;
-        const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-        grp = base + src;
-        row0 = __shfl_sync(0xffffffffu, r.row0, src);
-        row1 = __shfl_sync(0xffffffffu, r.row1, src);
-        break;
+    for (int base = 0; base < p.G && grp < 0; base += 256) {
+      const int g0 = base + 8 * lane;
+      int o[9], has = 0;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) o[i] = __ldg(p.off + min(g0 + i, p.G));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const RowRange r = held_inside(o[i], o[i + 1], p.M);
+        has += g0 + i < p.G && r.row1 > r.row0;
       }
-      want -= __popc(has);
+      int before = has;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += v;
+      }
+      const int total = __shfl_sync(0xffffffffu, before, 31);
+      if (want < total) {
+        before -= has;
+        int fg = -1, f0 = 0, f1 = 0, at = before;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const RowRange r = held_inside(o[i], o[i + 1], p.M);
+          if (g0 + i < p.G && r.row1 > r.row0) {
+            if (at == want) {
+              fg = g0 + i;
+              f0 = r.row0;
+              f1 = r.row1;
+            }
+            ++at;
+          }
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, fg >= 0)) - 1;
+        grp = __shfl_sync(0xffffffffu, fg, src);
+        row0 = __shfl_sync(0xffffffffu, f0, src);
+        row1 = __shfl_sync(0xffffffffu, f1, src);
+      }
+      want -= total;
     }
     if (grp < 0) return;  // the same for every warp of the CTA
   }
@@ -136,7 +165,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) fp8_small_kernel(const Fp8Ge
 #pragma unroll
       for (int q = 0; q < kKU; ++q) {
         const int kb = kb0 + q * kSmallWarps;
-        const int k0 = kb * kFp8Block + 32 * t;
+        const int k0 = kb * kFp8Block + 16 * t;
         const bool on = kb < p.KB;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
@@ -164,7 +193,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) fp8_small_kernel(const Fp8Ge
           // K ends inside this block: what lies behind it in the rows may be anything
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
-            const int left = p.K - (kb * kFp8Block + 32 * t + 4 * w);
+            const int left = p.K - (kb * kFp8Block + 64 * (w >> 2) + 16 * t + 4 * (w & 3));
 #pragma unroll
             for (int i = 0; i < kMT; ++i) {
               wb[q][i][0][w] = keep_bytes(wb[q][i][0][w], left);

@@ -1,0 +1,250 @@
+// fp8_stream.cuh - the block-scaled e4m3 product for groups of up to a few dozen
+// rows (experts of a canvas), where the time is the one read of the weights:
+//
+//   D[m, n] = w[m] * sum_kb sa[kb, m] * sb[n / 128, kb] * sum_{k in block kb} A[m, k] * B[n, k]
+//
+// Weights are the rows of the accumulator here: a unit is 128 features of one
+// group times a chunk of at most kTok of its tokens, so an instruction is as wide
+// as the tokens need (a multiple of 16 columns) and every copied byte of the
+// large operand is used.  On the pair kernel a group of 24 rows fills a tenth of
+// the 256 accumulator rows, its instructions take the time of 256, and the
+// stream of weights stops at 0.55 of the copy bandwidth.
+//
+// One CTA per SM, on its own.  Each stage holds one block of 128 k: 16 KB of
+// weights and the chunk's token rows (boxes of 16, 32 or kTok rows); eight
+// stages keep 128 KB of weights in flight, about three times what the latency of
+// HBM asks for.  Per block the MMA warp fills one of the tensor-memory buffers;
+// four epilogue warps (32 features each) add it, scaled, to a thread's kTok sums:
+// a column has its own token scale, read from shared memory, and the block's
+// weight scale is one number for the CTA.  A warp's store is 32 consecutive
+// features of one token.  Waits and their failure are as in fp8_gemm.cuh.
+#pragma once
+
+#include "fp8_gemm.cuh"
+
+namespace dg {
+
+constexpr int kStreamThreads = 256;  // warps: copies, MMAs, scales, idle, four of the epilogue
+
+template <int kTok>
+struct Fp8StreamShape {
+  static constexpr int kStages = 8, kBufs = 4, kScaleSlots = 4;
+  static constexpr int kStageA = 128 * 128, kStageB = kTok * 128;
+  static constexpr int kScaleSlot = 4 * kTok + 4;  // [4][kTok] token scales, [4] weight scales
+  static constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kScaleSlots + 1;
+  static constexpr int kSmem = 1024 + kStages * (kStageA + kStageB) + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
+};
+
+// tensor maps: weights with a box of 128 rows, tokens with boxes of 16, 32 and kTok rows
+struct Fp8StreamMaps {
+  CUtensorMap w;
+  CUtensorMap t[3];
+};
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int kTok, class TO>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    fp8_stream_kernel(const __grid_constant__ Fp8StreamMaps maps, const __grid_constant__ Fp8GemmParams p) {
+  using S = Fp8StreamShape<kTok>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ Fp8Tables tabs;
+  __shared__ int s_dead;
+  uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* const sA = smem;
+  uint8_t* const sB = sA + S::kStages * S::kStageA;
+  float* const s_scale = (float*)(sB + S::kStages * S::kStageB);
+  uint64_t* const bars = (uint64_t*)(s_scale + S::kScaleSlots * S::kScaleSlot);
+  uint32_t* const tmem_slot = (uint32_t*)(bars + S::kBars);
+  const uint32_t full = smem_u32(bars);                  // a stage's copies have landed
+  const uint32_t empty = full + 8 * S::kStages;          // its MMAs are done
+  const uint32_t acc_full = empty + 8 * S::kStages;      // a block's sums are in their buffer
+  const uint32_t acc_empty = acc_full + 8 * S::kBufs;    // the four epilogue warps have read it
+  const uint32_t sc_full = acc_empty + 8 * S::kBufs;
+  const uint32_t sc_empty = sc_full + 8 * S::kScaleSlots;
+  const uint32_t drain = sc_empty + 8 * S::kScaleSlots;
+  const uint32_t dead = smem_u32(&s_dead);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int b = 0; b < S::kBufs; ++b) {
+      mbar_init(acc_full + 8 * b, 1);
+      mbar_init(acc_empty + 8 * b, 4);
+    }
+    for (int i = 0; i < S::kScaleSlots; ++i) {
+      mbar_init(sc_full + 8 * i, 32);
+      mbar_init(sc_empty + 8 * i, 4);
+    }
+    mbar_init(drain, 1);
+    s_dead = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&maps.w);
+    for (int i = 0; i < 3; ++i) tma_prefetch_desc(&maps.t[i]);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), S::kBufs * kTok);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (p.off && warp == 4) fp8_tables<kTok>(p, &tabs, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int f_tiles = (p.N + 127) / 128;
+  const int chunks = p.off ? tabs.first[p.G] : (p.M + kTok - 1) / kTok;
+  const int U = f_tiles * chunks;
+  // unit u: a group's feature tiles one after the other, the chunks of a tile side by side
+  auto job = [&](int u) { return fp8_job<kTok>(p, &tabs, u, chunks, f_tiles, 128); };
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    uint32_t it = 0;
+    const uint64_t pol_w = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
+    const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
+    for (int u = blockIdx.x; u < U && !ld_shared_flag(dead); u += gridDim.x) {
+      const Fp8Job j = job(u);
+      const int rows = j.row1 - j.row0;
+      const int box = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
+      const uint32_t tx = (uint32_t)(128 + (box == 0 ? 16 : (box == 1 ? 32 : kTok))) * 128u;
+#pragma unroll 1
+      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+        const uint32_t s = it % S::kStages, bar = full + s * 8u;
+        wait_or_die(empty + s * 8u, ((it / S::kStages) & 1) ^ 1, dead);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, tx);
+          tma_load_2d_hint(dstA + s * S::kStageA, &maps.w, bar, kb * 128, j.group * p.N + j.n0, pol_w);
+          tma_load_2d_hint(dstB + s * S::kStageB, &maps.t[box], bar, kb * 128, j.row0, pol_t);
+        }
+        __syncwarp();
+      }
+    }
+    const uint32_t first = it > (uint32_t)S::kStages ? it - S::kStages : 0;
+    for (uint32_t q = first; q < it; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    uint32_t it = 0;
+    const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
+    for (int u = blockIdx.x; u < U && !ld_shared_flag(dead); u += gridDim.x) {
+      const Fp8Job j = job(u);
+      const uint32_t idesc = idesc_e4m3_f32(128, (j.row1 - j.row0 + 15) & ~15);
+#pragma unroll 1
+      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+        const uint32_t s = it % S::kStages, b = it % S::kBufs;
+        wait_or_die(acc_empty + b * 8u, ((it / S::kBufs) & 1) ^ 1, dead);
+        wait_or_die(full + s * 8u, (it / S::kStages) & 1, dead);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t da = descA + s * (S::kStageA / 16), db = descB + s * (S::kStageB / 16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_e4m3(tmem_base + b * kTok, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+          umma_commit(empty + s * 8u);
+          umma_commit(acc_full + b * 8u);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(drain);
+    wait_or_die(drain, 0, dead);
+  } else if (warp == 2) {
+    // ---------------- scales: four blocks per slot ----------------
+    uint32_t batch = 0;
+    for (int u = blockIdx.x; u < U && !ld_shared_flag(dead); u += gridDim.x) {
+      const Fp8Job j = job(u);
+      const float* const sb = p.sb + ((long long)j.group * p.NB + j.n0 / kFp8Block) * p.KB;
+#pragma unroll 1
+      for (int kb0 = 0; kb0 < p.KB; kb0 += 4, ++batch) {
+        const uint32_t slot = batch % S::kScaleSlots;
+        wait_or_die(sc_empty + slot * 8u, ((batch / S::kScaleSlots) & 1) ^ 1, dead);
+        const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* const src = p.sa + (long long)min(kb0 + q, p.KB - 1) * p.lds;
+#pragma unroll
+          for (int i = 0; i < kTok / 32; ++i)
+            cp_async4(dst + (uint32_t)(q * kTok + 32 * i + lane) * 4u, src + min(j.row0 + 32 * i + lane, j.row1 - 1));
+        }
+        if (lane < 4) cp_async4(dst + (uint32_t)(4 * kTok + lane) * 4u, sb + min(kb0 + lane, p.KB - 1));
+        cp_async_arrive(sc_full + slot * 8u);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 4) {
+    // ---------------- epilogue: features [32 quarter, +32) ----------------
+    const int quarter = warp & 3;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    uint32_t it = 0, batch = 0;
+    for (int u = blockIdx.x; u < U; u += gridDim.x) {
+      const Fp8Job j = job(u);
+      const int n_ld = (j.row1 - j.row0 + 31) / 32;  // 32-token parts
+      float acc[kTok];
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) acc[i] = 0.f;
+#pragma unroll 1
+      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+        const uint32_t slot = batch % S::kScaleSlots, b = it % S::kBufs;
+        if ((kb & 3) == 0) wait_or_die(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead);
+        const uint32_t at = smem_u32(s_scale + slot * S::kScaleSlot);
+        const float sb = __int_as_float(ld_shared_flag(at + (uint32_t)(4 * kTok + (kb & 3)) * 4u));
+        wait_or_die(acc_full + b * 8u, (it / S::kBufs) & 1, dead);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kTok / 32; ++c) {
+          if (c < n_ld) {
+            uint32_t r[32];
+            tmem_ld32_nowait(lane_base + b * kTok + c * 32, r);
+            tmem_wait32(r);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 sa = ld_shared_f4(at + (uint32_t)((kb & 3) * kTok + c * 32 + i) * 4u);
+              acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sa.x * sb, acc[c * 32 + i]);
+              acc[c * 32 + i + 1] = fmaf(__uint_as_float(r[i + 1]), sa.y * sb, acc[c * 32 + i + 1]);
+              acc[c * 32 + i + 2] = fmaf(__uint_as_float(r[i + 2]), sa.z * sb, acc[c * 32 + i + 2]);
+              acc[c * 32 + i + 3] = fmaf(__uint_as_float(r[i + 3]), sa.w * sb, acc[c * 32 + i + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + b * 8u);
+        if ((kb & 3) == 3 || kb + 1 == p.KB) {
+          if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+          ++batch;
+        }
+      }
+      const bool bad = ld_shared_flag(dead) != 0;  // a wait ran out: what was added is not the product
+      const int n = j.n0 + quarter * 32 + lane;
+      TO* const o = static_cast<TO*>(p.out) + (long long)j.row0 * p.ldo + n;
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        if (j.row0 + i < j.row1 && n < p.N) {
+          float v = bad ? __uint_as_float(0x7fffffffu) : acc[i];
+          if (p.row_w) v *= __ldg(p.row_w + j.row0 + i);
+          store_out(o + (long long)i * p.ldo, v);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, S::kBufs * kTok);
+}
+
+}  // namespace dg
