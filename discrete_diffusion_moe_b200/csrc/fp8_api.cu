@@ -122,10 +122,11 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
   const int rows[3] = {16, 32, kTok};
   DG_TRY(make_tmap_codes(&maps.w, p.b, p.K, (long long)p.G * p.N, p.ldb, 128));
   for (int i = 0; i < 3; ++i) DG_TRY(make_tmap_codes(&maps.t[i], p.a, p.K, p.M, p.lda, rows[i]));
-  DG_TRY(set_smem_attr((const void*)fp8_stream_kernel<kTok, TO>, S::kSmem, true));
+  DG_TRY(set_smem_attr((const void*)fp8_stream_kernel<kTok, TO>, S::smem(kFp8MaxGroups), true));
+  const int smem = S::smem(p.G), ctas = smem <= 113 * 1024 ? 2 : 1;  // of an SM's 228 KB, 1 KB of each CTA reserved
   const long long chunks = p.off ? std::min(p.G, p.M) + (long long)p.M / kTok : ceil_div(p.M, kTok);  // at most
-  const unsigned grid = (unsigned)std::min<long long>(sms, chunks * ceil_div(p.N, 128));
-  DG_CUDA(Launch(dim3(grid), dim3(kStreamThreads), S::kSmem, st)(fp8_stream_kernel<kTok, TO>, maps, p));
+  const unsigned grid = (unsigned)std::min<long long>(ctas * sms, chunks * ceil_div(p.N, 128));
+  DG_CUDA(Launch(dim3(grid), dim3(kStreamThreads), smem, st)(fp8_stream_kernel<kTok, TO>, maps, p));
   return DG_OK;
 }
 

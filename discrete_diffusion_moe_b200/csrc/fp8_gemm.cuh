@@ -156,14 +156,15 @@ struct Fp8Maps {
 };
 
 struct Fp8Tables {
-  int first[kFp8MaxGroups + 1];  // row tiles of the groups before g
-  int row0[kFp8MaxGroups];
-  int row1[kFp8MaxGroups];
+  int* first;  // [groups + 1] row tiles of the groups before g
+  int* row0;   // [groups]
+  int* row1;
+  __device__ Fp8Tables(int* at, int groups) : first(at), row0(at + groups + 1), row1(at + 2 * groups + 1) {}
 };
 
 // The groups' rows and their prefix sums of tiles of kRows rows (one warp).
 template <int kRows>
-__device__ __forceinline__ void fp8_tables(const Fp8GemmParams& p, Fp8Tables* tb, int lane) {
+__device__ __forceinline__ void fp8_tables(const Fp8GemmParams& p, const Fp8Tables& tb, int lane) {
   int sum = 0;
   for (int base = 0; base < p.G; base += 32) {
     const int g = base + lane;
@@ -177,13 +178,13 @@ __device__ __forceinline__ void fp8_tables(const Fp8GemmParams& p, Fp8Tables* tb
       if (lane >= o) inc += v;
     }
     if (g < p.G) {
-      tb->first[g] = sum + inc - t;
-      tb->row0[g] = r.row0;
-      tb->row1[g] = r.row1;
+      tb.first[g] = sum + inc - t;
+      tb.row0[g] = r.row0;
+      tb.row1[g] = r.row1;
     }
     sum += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (lane == 0) tb->first[p.G] = sum;
+  if (lane == 0) tb.first[p.G] = sum;
 }
 
 struct Fp8Job {
@@ -194,7 +195,7 @@ struct Fp8Job {
 // tiles (all groups together); a group's row tiles of one column tile are
 // consecutive units, which share their columns of B.
 template <int kRows>
-__device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Tables* tb, int u, int m_tiles, int n_tiles,
+__device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Tables& tb, int u, int m_tiles, int n_tiles,
                                           int bn) {
   Fp8Job j;
   if (!p.off) {
@@ -208,15 +209,15 @@ __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Table
   int lo = 0, hi = p.G;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (tb->first[mid] * n_tiles <= u) lo = mid;
+    if (tb.first[mid] * n_tiles <= u) lo = mid;
     else hi = mid;
   }
-  const int tiles = tb->first[lo + 1] - tb->first[lo];
-  const int r = u - tb->first[lo] * n_tiles;
+  const int tiles = tb.first[lo + 1] - tb.first[lo];
+  const int r = u - tb.first[lo] * n_tiles;
   const int nt = r / tiles, mt = r - nt * tiles;
   j.group = lo;
-  j.row0 = tb->row0[lo] + mt * kRows;
-  j.row1 = min(tb->row1[lo], j.row0 + kRows);
+  j.row0 = tb.row0[lo] + mt * kRows;
+  j.row1 = min(tb.row1[lo], j.row0 + kRows);
   j.n0 = nt * bn;
   return j;
 }
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8GemmParams p) {
   using S = Fp8Shape<kW>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ Fp8Tables tabs;
+  __shared__ int s_tabs[3 * kFp8MaxGroups + 1];
+  const Fp8Tables tabs(s_tabs, kFp8MaxGroups);
   __shared__ int s_dead;
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const sA = smem;
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   grid_dep_wait();
   grid_dep_launch();
   int m_tiles = (p.M + 255) / 256;
-  if (p.off && warp == 4) fp8_tables<256>(p, &tabs, lane);
+  if (p.off && warp == 4) fp8_tables<256>(p, tabs, lane);
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers initialised before either signals one
   if (warp == 1) {
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       auto a_box = [&](int rows) { return rows <= 0 ? -1 : (rows <= 16 ? 0 : (rows <= 64 ? 1 : 2)); };
       auto a_bytes = [&](int box) { return box < 0 ? 0u : (box == 0 ? 16u : (box == 1 ? 64u : 128u)) * 128u; };
       for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
-        const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
+        const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
         const int mine = a_box(j.row1 - (j.row0 + (int)rank * 128));
         uint32_t tx = a_bytes(a_box(j.row1 - j.row0)) + a_bytes(a_box(j.row1 - j.row0 - 128));
         const int n = mma_cols(j);
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         int kb = (int)m;  // block of this warp within the unit
         const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
         for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
-          const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
+          const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
           const uint32_t idesc = idesc_e4m3_f32(256, mma_cols(j));
 #pragma unroll 1
           for (; kb < p.KB; kb += 2) {
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // asking for the next set the pace of the whole kernel (950 cycles per block).
       uint32_t slot = 0, phase = 1;
       for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
-        const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
+        const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
         const float* src[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) src[i] = p.sa + min(j.row0 + (int)rank * 128 + 32 * i + lane, j.row1 - 1);
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const float4* const my_sb = reinterpret_cast<const float4*>(s_scale) + 128 + half;
     uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0, turn_next = 0;
     for (int u = pair; u < U; u += pairs) {
-      const Fp8Job j = fp8_job<256>(p, &tabs, u, m_tiles, n_tiles, kW);
+      const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
       const int col = j.n0 + half * S::kCols;
       const bool work = row_w0 < j.row1 && col < p.N;

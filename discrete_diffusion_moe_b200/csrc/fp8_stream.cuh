@@ -10,9 +10,10 @@
 // the 256 accumulator rows, its instructions take the time of 256, and the
 // stream of weights stops at 0.55 of the copy bandwidth.
 //
-// One CTA per SM, on its own.  Each stage holds one block of 128 k: 16 KB of
-// weights and the chunk's token rows (boxes of 16, 32 or kTok rows); eight
-// stages keep 128 KB of weights in flight, about three times what the latency of
+// Two CTAs per SM, each on its own, so that one's waits and stores are covered by
+// the other.  Each stage holds one block of 128 k: 16 KB of weights and the
+// chunk's token rows (boxes of 16, 32 or kTok rows); four stages in either CTA
+// keep 128 KB of weights in flight per SM, about three times what the latency of
 // HBM asks for.  Per block the MMA warp fills one of the tensor-memory buffers;
 // four epilogue warps (32 features each) add it, scaled, to a thread's kTok sums:
 // a column has its own token scale, read from shared memory, and the block's
@@ -28,11 +29,12 @@ constexpr int kStreamThreads = 256;  // warps: copies, MMAs, scales, idle, four 
 
 template <int kTok>
 struct Fp8StreamShape {
-  static constexpr int kStages = 8, kBufs = 4, kScaleSlots = 4;
+  static constexpr int kStages = 4, kBufs = 4, kScaleSlots = 4;
   static constexpr int kStageA = 128 * 128, kStageB = kTok * 128;
   static constexpr int kScaleSlot = 4 * kTok + 4;  // [4][kTok] token scales, [4] weight scales
   static constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kScaleSlots + 1;
-  static constexpr int kSmem = 1024 + kStages * (kStageA + kStageB) + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
+  static constexpr int kFixed = 1024 + kStages * (kStageA + kStageB) + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
+  static constexpr int smem(int groups) { return kFixed + 4 * (3 * groups + 1); }  // with the groups' tables
 };
 
 // tensor maps: weights with a box of 128 rows, tokens with boxes of 16, 32 and kTok rows
@@ -52,11 +54,10 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
 }
 
 template <int kTok, class TO>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+__global__ void __launch_bounds__(kStreamThreads, 2)
     fp8_stream_kernel(const __grid_constant__ Fp8StreamMaps maps, const __grid_constant__ Fp8GemmParams p) {
   using S = Fp8StreamShape<kTok>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ Fp8Tables tabs;
   __shared__ int s_dead;
   uint8_t* const smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const sA = smem;
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   float* const s_scale = (float*)(sB + S::kStages * S::kStageB);
   uint64_t* const bars = (uint64_t*)(s_scale + S::kScaleSlots * S::kScaleSlot);
   uint32_t* const tmem_slot = (uint32_t*)(bars + S::kBars);
+  const Fp8Tables tabs((int*)(tmem_slot + 4), p.G);
   const uint32_t full = smem_u32(bars);                  // a stage's copies have landed
   const uint32_t empty = full + 8 * S::kStages;          // its MMAs are done
   const uint32_t acc_full = empty + 8 * S::kStages;      // a block's sums are in their buffer
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
   grid_dep_wait();
   grid_dep_launch();
-  if (p.off && warp == 4) fp8_tables<kTok>(p, &tabs, lane);
+  if (p.off && warp == 4) fp8_tables<kTok>(p, tabs, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int chunks = p.off ? tabs.first[p.G] : (p.M + kTok - 1) / kTok;
   const int U = f_tiles * chunks;
   // unit u: a group's feature tiles one after the other, the chunks of a tile side by side
-  auto job = [&](int u) { return fp8_job<kTok>(p, &tabs, u, chunks, f_tiles, 128); };
+  auto job = [&](int u) { return fp8_job<kTok>(p, tabs, u, chunks, f_tiles, 128); };
 
   if (warp == 0) {
     // ---------------- copies ----------------
