@@ -14,8 +14,11 @@
 
 using namespace dg;
 
+#ifndef FP8_SMALL_ROWS
+#define FP8_SMALL_ROWS 16
+#endif
 #ifndef FP8_STREAM_ROWS
-#define FP8_STREAM_ROWS 64
+#define FP8_STREAM_ROWS 80
 #endif
 namespace {
 
@@ -125,17 +128,21 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
   DG_TRY(set_smem_attr((const void*)fp8_stream_kernel<kTok, TO>, S::smem(kFp8MaxGroups), true));
   const int smem = S::smem(p.G), ctas = smem <= 113 * 1024 ? 2 : 1;  // of an SM's 228 KB, 1 KB of each CTA reserved
   const long long chunks = p.off ? std::min(p.G, p.M) + (long long)p.M / kTok : ceil_div(p.M, kTok);  // at most
-  const unsigned grid = (unsigned)std::min<long long>(ctas * sms, chunks * ceil_div(p.N, 128));
-  DG_CUDA(Launch(dim3(grid), dim3(kStreamThreads), smem, st)(fp8_stream_kernel<kTok, TO>, maps, p));
+  const long long units = chunks * ceil_div(p.N, 128), slots = (long long)ctas * sms;
+  // few units: split each one's blocks, two at least to a CTA, among a cluster
+  const int splits = (int)std::max<long long>(1, std::min<long long>({slots / units, 8, p.KB / 2}));
+  Launch l(dim3((unsigned)(splits > 1 ? splits * units : std::min(units, slots))), dim3(kStreamThreads), smem, st);
+  if (splits > 1) l.cluster((unsigned)splits, 1, 1);
+  DG_CUDA(l(fp8_stream_kernel<kTok, TO>, maps, p, splits));
   return DG_OK;
 }
 
 template <class TO>
 dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
-  if (p.M <= 16) return launch_small<TO>(p, st);
+  if (p.M <= FP8_SMALL_ROWS) return launch_small<TO>(p, st);
   const int sms = device_sms(), pairs = sms / 2;
   const long long groups = p.off ? std::min(p.G, p.M) : 1;  // that may have rows
-  if (p.M <= FP8_STREAM_ROWS * groups && groups * ceil_div(p.N, 128) >= sms) return launch_stream<64, TO>(p, sms, st);
+  if (p.M <= FP8_STREAM_ROWS * groups) return launch_stream<64, TO>(p, sms, st);
   const long long tiles = p.off ? std::max<long long>(groups, p.M / 256) : ceil_div(p.M, 256);
   if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<256, TO>(p, pairs, st);
   if (tiles * ceil_div(p.N, 128) >= pairs / 2) return launch_pair<128, TO>(p, pairs, st);

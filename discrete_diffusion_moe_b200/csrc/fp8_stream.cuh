@@ -19,6 +19,10 @@
 // a column has its own token scale, read from shared memory, and the block's
 // weight scale is one number for the CTA.  A warp's store is 32 consecutive
 // features of one token.  Waits and their failure are as in fp8_gemm.cuh.
+//
+// Where there are fewer units than CTAs (single tokens) the blocks of a unit are
+// split among the CTAs of a cluster: each leaves its sums in its shared memory
+// (the stages, free by then), and the first adds them in the order of the ranks.
 #pragma once
 
 #include "fp8_gemm.cuh"
@@ -53,9 +57,16 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
+__device__ __forceinline__ float ld_dsmem_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 template <int kTok, class TO>
 __global__ void __launch_bounds__(kStreamThreads, 2)
-    fp8_stream_kernel(const __grid_constant__ Fp8StreamMaps maps, const __grid_constant__ Fp8GemmParams p) {
+    fp8_stream_kernel(const __grid_constant__ Fp8StreamMaps maps, const __grid_constant__ Fp8GemmParams p,
+                      const int splits) {
   using S = Fp8StreamShape<kTok>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_dead;
@@ -75,6 +86,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   const uint32_t drain = sc_empty + 8 * S::kScaleSlots;
   const uint32_t dead = smem_u32(&s_dead);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // splits > 1: one unit per cluster, this CTA takes blocks [kb0, kb1)
+  const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
+  const int first = (int)blockIdx.x / splits, stride = (int)gridDim.x / splits;
+  const int kb_lo = p.KB * rank / splits, kb_hi = p.KB * (rank + 1) / splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -118,13 +133,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     uint32_t it = 0;
     const uint64_t pol_w = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
     const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
-    for (int u = blockIdx.x; u < U && !ld_shared_flag(dead); u += gridDim.x) {
+    for (int u = first; u < U && !ld_shared_flag(dead); u += stride) {
       const Fp8Job j = job(u);
       const int rows = j.row1 - j.row0;
       const int box = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
       const uint32_t tx = (uint32_t)(128 + (box == 0 ? 16 : (box == 1 ? 32 : kTok))) * 128u;
 #pragma unroll 1
-      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t s = it % S::kStages, bar = full + s * 8u;
         wait_or_die(empty + s * 8u, ((it / S::kStages) & 1) ^ 1, dead);
         if (elect_one()) {
@@ -135,17 +150,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         __syncwarp();
       }
     }
-    const uint32_t first = it > (uint32_t)S::kStages ? it - S::kStages : 0;
-    for (uint32_t q = first; q < it; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
+    for (uint32_t q = it > (uint32_t)S::kStages ? it - S::kStages : 0; q < it; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     uint32_t it = 0;
     const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
-    for (int u = blockIdx.x; u < U && !ld_shared_flag(dead); u += gridDim.x) {
+    for (int u = first; u < U && !ld_shared_flag(dead); u += stride) {
       const Fp8Job j = job(u);
       const uint32_t idesc = idesc_e4m3_f32(128, (j.row1 - j.row0 + 15) & ~15);
 #pragma unroll 1
-      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t s = it % S::kStages, b = it % S::kBufs;
         wait_or_die(acc_empty + b * 8u, ((it / S::kBufs) & 1) ^ 1, dead);
         wait_or_die(full + s * 8u, (it / S::kStages) & 1, dead);
@@ -166,11 +180,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   } else if (warp == 2) {
     // ---------------- scales: four blocks per slot ----------------
     uint32_t batch = 0;
-    for (int u = blockIdx.x; u < U && !ld_shared_flag(dead); u += gridDim.x) {
+    for (int u = first; u < U && !ld_shared_flag(dead); u += stride) {
       const Fp8Job j = job(u);
       const float* const sb = p.sb + ((long long)j.group * p.NB + j.n0 / kFp8Block) * p.KB;
 #pragma unroll 1
-      for (int kb0 = 0; kb0 < p.KB; kb0 += 4, ++batch) {
+      for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += 4, ++batch) {
         const uint32_t slot = batch % S::kScaleSlots;
         wait_or_die(sc_empty + slot * 8u, ((batch / S::kScaleSlots) & 1) ^ 1, dead);
         const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
@@ -191,18 +205,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     const int quarter = warp & 3;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     uint32_t it = 0, batch = 0;
-    for (int u = blockIdx.x; u < U; u += gridDim.x) {
+    for (int u = first; u < U; u += stride) {
       const Fp8Job j = job(u);
       const int n_ld = (j.row1 - j.row0 + 31) / 32;  // 32-token parts
       float acc[kTok];
 #pragma unroll
       for (int i = 0; i < kTok; ++i) acc[i] = 0.f;
 #pragma unroll 1
-      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t slot = batch % S::kScaleSlots, b = it % S::kBufs;
-        if ((kb & 3) == 0) wait_or_die(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead);
+        const int q = (kb - kb_lo) & 3;
+        if (q == 0) wait_or_die(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead);
         const uint32_t at = smem_u32(s_scale + slot * S::kScaleSlot);
-        const float sb = __int_as_float(ld_shared_flag(at + (uint32_t)(4 * kTok + (kb & 3)) * 4u));
+        const float sb = __int_as_float(ld_shared_flag(at + (uint32_t)(4 * kTok + q) * 4u));
         wait_or_die(acc_full + b * 8u, (it / S::kBufs) & 1, dead);
         tc_fence_after();
 #pragma unroll
@@ -213,7 +228,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             tmem_wait32(r);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 sa = ld_shared_f4(at + (uint32_t)((kb & 3) * kTok + c * 32 + i) * 4u);
+              const float4 sa = ld_shared_f4(at + (uint32_t)(q * kTok + c * 32 + i) * 4u);
               acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), sa.x * sb, acc[c * 32 + i]);
               acc[c * 32 + i + 1] = fmaf(__uint_as_float(r[i + 1]), sa.y * sb, acc[c * 32 + i + 1]);
               acc[c * 32 + i + 2] = fmaf(__uint_as_float(r[i + 2]), sa.z * sb, acc[c * 32 + i + 2]);
@@ -224,17 +239,24 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + b * 8u);
-        if ((kb & 3) == 3 || kb + 1 == p.KB) {
+        if (q == 3 || kb + 1 == kb_hi) {
           if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
           ++batch;
         }
       }
+      const int f = quarter * 32 + lane, n = j.n0 + f, rows = j.row1 - j.row0;
+      if (splits > 1) {  // added and stored below, when the whole cluster has come there
+        float* const sums = reinterpret_cast<float*>(smem);  // every copy into the stages has been used
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+          if (i < rows) sums[i * 128 + f] = ld_shared_flag(dead) ? __uint_as_float(0x7fffffffu) : acc[i];
+        continue;
+      }
       const bool bad = ld_shared_flag(dead) != 0;  // a wait ran out: what was added is not the product
-      const int n = j.n0 + quarter * 32 + lane;
       TO* const o = static_cast<TO*>(p.out) + (long long)j.row0 * p.ldo + n;
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
-        if (j.row0 + i < j.row1 && n < p.N) {
+        if (i < rows && n < p.N) {
           float v = bad ? __uint_as_float(0x7fffffffu) : acc[i];
           if (p.row_w) v *= __ldg(p.row_w + j.row0 + i);
           store_out(o + (long long)i * p.ldo, v);
@@ -247,6 +269,21 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, S::kBufs * kTok);
+  if (splits > 1) {
+    cluster_sync_all();  // every CTA's sums are written
+    if (first < U) {
+      // token i is added up (in the order of the ranks) and stored by CTA i % splits
+      const Fp8Job j = job(first);
+      const int f = threadIdx.x & 127, n = j.n0 + f, rows = j.row1 - j.row0;
+      for (int i = rank + splits * (int)(threadIdx.x >> 7); i < rows; i += 2 * splits) {
+        float v = 0.f;
+        for (int r = 0; r < splits; ++r) v += ld_dsmem_f1(mapa_shared(smem_u32(smem) + (uint32_t)(i * 128 + f) * 4u, (uint32_t)r));
+        if (p.row_w) v *= __ldg(p.row_w + j.row0 + i);
+        if (n < p.N) store_out(static_cast<TO*>(p.out) + (long long)(j.row0 + i) * p.ldo + n, v);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its shared memory
+  }
 }
 
 }  // namespace dg
