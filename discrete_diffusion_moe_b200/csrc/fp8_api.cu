@@ -14,12 +14,6 @@
 
 using namespace dg;
 
-#ifndef FP8_SMALL_ROWS
-#define FP8_SMALL_ROWS 16
-#endif
-#ifndef FP8_STREAM_ROWS
-#define FP8_STREAM_ROWS 80
-#endif
 namespace {
 
 constexpr long long kMaxDim = 2147483647ll;
@@ -57,10 +51,8 @@ dg_status launch_quant_blocks(const QuantBlocksParams& p, long long blocks, bool
 
 template <class TO>
 dg_status launch_small(const Fp8GemmParams& p, cudaStream_t st) {
-  const unsigned slots = p.off ? (unsigned)std::min(p.G, p.M) : 1u;
-  const dim3 grid((unsigned)ceil_div(p.N, 16), slots);
-  if (p.M <= 8) DG_CUDA(Launch(grid, dim3(32 * kSmallWarps), 0, st)(fp8_small_kernel<1, 1, 3, TO>, p));
-  else          DG_CUDA(Launch(grid, dim3(32 * kSmallWarps), 0, st)(fp8_small_kernel<1, 2, 2, TO>, p));
+  const dim3 grid((unsigned)ceil_div(p.N, 16), p.off ? (unsigned)std::min(p.G, p.M) : 1u);
+  DG_CUDA(Launch(grid, dim3(32 * kSmallWarps), 0, st)(fp8_small_kernel<TO>, p));
   return DG_OK;
 }
 
@@ -137,16 +129,25 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
   return DG_OK;
 }
 
+// Which kernel, by rows and columns (times of K = 2816, bf16 out, in us):
+//   at most 8 rows and two waves of its CTAs: mma.sync, where the set-up counts
+//     (one token, 5632 features: 6.3, streaming 9.4; 262144 features: 186, 111);
+//   at most 80 rows a group on average: the streaming kernel (1408 features, 128
+//     experts, 8192 rows: 130, pairs 154; 16384 rows: 223, 171);
+//   else CTA pairs, with the widest tile that still gives about every pair work
+//     (narrower tiles read A more often: 256 rows of 5632 features with 128
+//     columns a tile 13.5, with 64 14.9).
+constexpr int kStreamRows = 80;
+
 template <class TO>
 dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
-  if (p.M <= FP8_SMALL_ROWS) return launch_small<TO>(p, st);
   const int sms = device_sms(), pairs = sms / 2;
   const long long groups = p.off ? std::min(p.G, p.M) : 1;  // that may have rows
-  if (p.M <= FP8_STREAM_ROWS * groups) return launch_stream<64, TO>(p, sms, st);
+  if (p.M <= kSmallRows && groups * ceil_div(p.N, 16) <= 2ll * kSmallCtas * sms) return launch_small<TO>(p, st);
+  if (p.M <= kStreamRows * groups) return launch_stream<64, TO>(p, sms, st);
   const long long tiles = p.off ? std::max<long long>(groups, p.M / 256) : ceil_div(p.M, 256);
   if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<256, TO>(p, pairs, st);
-  if (tiles * ceil_div(p.N, 128) >= pairs / 2) return launch_pair<128, TO>(p, pairs, st);
-  return launch_pair<64, TO>(p, pairs, st);
+  return launch_pair<128, TO>(p, pairs, st);
 }
 
 dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, cudaStream_t st) {

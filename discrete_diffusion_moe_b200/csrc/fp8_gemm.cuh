@@ -287,7 +287,9 @@ __device__ __forceinline__ void store_turned(uint8_t* turn, const CUtensorMap* m
       }
       *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    if (map) {
+    // the copy engine clips rows of whole 16-byte units only: where the matrix ends
+    // inside one it wrote zeros up to the unit's end
+    if (map && (c0 + kPass <= cols || cols % kUnit == 0)) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {

@@ -1,20 +1,23 @@
-// fp8_small.cuh - the block-scaled e4m3 product for few rows (single tokens,
-// experts with a handful of tokens):
+// fp8_small.cuh - the block-scaled e4m3 product for at most eight rows and few
+// features (a token's projections, its experts), where latency counts:
 //
 //   D[m, n] = w[m] * sum_kb sa[kb, m] * sb[n / 128, kb] * sum_{k in block kb} A[m, k] * B[n, k]
 //
 // A: activation codes [M, K], B: weight codes [N, K] (or [G, N, K] with the rows
-// of A split among the groups).  The time is the one read of B.
+// of A split among the groups).  The time is a launch and the one read of B.
 //
-// mma.sync m16n8k32 with 16 weight rows as its M side and 8 tokens as its N
-// side: a tcgen05 tile would spend 128 rows on one token, and here the weights
-// go from global memory to registers without a stop in shared memory.  The
-// order of k inside a block is free as long as A and B agree, so lane (g, t)
-// of a warp takes bytes [16 t, 16 t + 16) of both halves of its rows' 128: two
-// 16-byte loads per row, each of whole sectors, and four products per block.  The eight warps of a CTA
-// share its features and take every eighth block of K each: all of a CTA's
-// loads are in flight together.  Their fp32 partial sums meet in shared memory
-// in the order of the warps (the result does not depend on timing).
+// mma.sync m16n8k32 with 16 weight rows as its M side and the tokens as its N
+// side: no tensor memory, tensor maps or barriers to set up (the streaming
+// tcgen05 kernel starts about 3 us later), and the weights go from global memory
+// to registers.  The order of k inside a block is free as long as A and B agree,
+// so lane (g, t) of a warp takes bytes [16 t, 16 t + 16) of both halves of its
+// rows' 128: two 16-byte loads per row, each of whole sectors, and four products
+// per block.  The eight warps of a CTA share its 16 features and take every
+// eighth block of K each.  One block per warp is in flight, and 48 registers let
+// five CTAs share an SM: with three blocks in flight and two CTAs 5632 features
+// of one token took 7.7 us (two waves), so 6.3; 8 experts 14.0, so 10.4.  The
+// warps' fp32 sums meet in shared memory in the order of the warps (the result
+// does not depend on timing).
 #pragma once
 
 #include "common.cuh"
@@ -87,13 +90,11 @@ __device__ __forceinline__ void load_codes32(uint32_t (&w)[8], const uint8_t* ro
   }
 }
 
-constexpr int kSmallWarps = 8;
+constexpr int kSmallWarps = 8, kSmallRows = 8, kSmallCtas = 5;  // CTAs per SM
 
-// kMT 16-feature tiles and kNT 8-token tiles per CTA, kKU blocks of K loaded
-// together by each warp.
-template <int kMT, int kNT, int kKU, class TO>
-__global__ void __launch_bounds__(32 * kSmallWarps) fp8_small_kernel(const Fp8GemmParams p) {
-  constexpr int kFeat = 16 * kMT, kTok = 8 * kNT;
+template <class TO>
+__global__ void __launch_bounds__(32 * kSmallWarps, kSmallCtas) fp8_small_kernel(const Fp8GemmParams p) {
+  constexpr int kFeat = 16, kTok = kSmallRows;
   __shared__ float red[kSmallWarps][kTok][kFeat + 1];
   grid_dep_wait();
   grid_dep_launch();
@@ -151,80 +152,42 @@ __global__ void __launch_bounds__(32 * kSmallWarps) fp8_small_kernel(const Fp8Ge
   const float* const sb = p.sb + ((long long)grp * p.NB + n0 / kFp8Block) * p.KB;
 
   for (int m0 = row0; m0 < row1; m0 += kTok) {
-    float acc[kMT][kNT][4];
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int kb = warp; kb < p.KB; kb += kSmallWarps) {
+      const int k0 = kb * kFp8Block + 16 * t;
+      uint32_t wb[2][8], wa[8];
+      float sc[2];
 #pragma unroll
-    for (int i = 0; i < kMT; ++i)
+      for (int h = 0; h < 2; ++h) {
+        const int n = n0 + 8 * h + g;
+        load_codes32<true>(wb[h], b + (long long)n * p.ldb, k0, p.K, n < p.N);
+      }
+      load_codes32<false>(wa, p.a + (long long)(m0 + g) * p.lda, k0, p.K, m0 + g < row1);
 #pragma unroll
-      for (int j = 0; j < kNT; ++j)
+      for (int e = 0; e < 2; ++e) {
+        const int mc = m0 + 2 * t + e;
+        sc[e] = mc < row1 ? __ldg(p.sa + (long long)kb * p.lds + mc) * __ldg(sb + kb) : 0.f;
+      }
+      if ((kb + 1) * kFp8Block > p.K) {
+        // K ends inside this block: what lies behind it in the rows may be anything
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-
-    for (int kb0 = warp; kb0 < p.KB; kb0 += kSmallWarps * kKU) {
-      uint32_t wb[kKU][kMT][2][8], wa[kKU][kNT][8];
-      float sc[kKU][kNT][2];
-#pragma unroll
-      for (int q = 0; q < kKU; ++q) {
-        const int kb = kb0 + q * kSmallWarps;
-        const int k0 = kb * kFp8Block + 16 * t;
-        const bool on = kb < p.KB;
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n = n0 + 16 * i + 8 * h + g;
-            load_codes32<true>(wb[q][i][h], b + (long long)n * p.ldb, k0, p.K, on && n < p.N);
-          }
-#pragma unroll
-        for (int j = 0; j < kNT; ++j) {
-          const int m = m0 + 8 * j + g;
-          load_codes32<false>(wa[q][j], p.a + (long long)m * p.lda, k0, p.K, on && m < row1);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int mc = m0 + 8 * j + 2 * t + e;
-            sc[q][j][e] = on && mc < row1 ? __ldg(p.sa + (long long)kb * p.lds + mc) * __ldg(sb + kb) : 0.f;
-          }
+        for (int w = 0; w < 8; ++w) {
+          const int left = p.K - (k0 + 64 * (w >> 2) + 4 * (w & 3));
+          wb[0][w] = keep_bytes(wb[0][w], left);
+          wb[1][w] = keep_bytes(wb[1][w], left);
+          wa[w] = keep_bytes(wa[w], left);
         }
       }
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < kKU; ++q) {
-        const int kb = kb0 + q * kSmallWarps;
-        if (kb >= p.KB) break;
-        if ((kb + 1) * kFp8Block > p.K) {
-          // K ends inside this block: what lies behind it in the rows may be anything
+      for (int s = 0; s < 4; ++s)
+        mma_e4m3(c, wb[0][2 * s], wb[1][2 * s], wb[0][2 * s + 1], wb[1][2 * s + 1], wa[2 * s], wa[2 * s + 1]);
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const int left = p.K - (kb * kFp8Block + 64 * (w >> 2) + 16 * t + 4 * (w & 3));
-#pragma unroll
-            for (int i = 0; i < kMT; ++i) {
-              wb[q][i][0][w] = keep_bytes(wb[q][i][0][w], left);
-              wb[q][i][1][w] = keep_bytes(wb[q][i][1][w], left);
-            }
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) wa[q][j][w] = keep_bytes(wa[q][j][w], left);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kMT; ++i)
-#pragma unroll
-          for (int j = 0; j < kNT; ++j) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_e4m3(c, wb[q][i][0][2 * s], wb[q][i][1][2 * s], wb[q][i][0][2 * s + 1], wb[q][i][1][2 * s + 1],
-                       wa[q][j][2 * s], wa[q][j][2 * s + 1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(c[e], sc[q][j][e & 1], acc[i][j][e]);
-          }
-      }
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], sc[e & 1], acc[e]);
     }
-    // accumulator (i, j): features 16 i + g (e 0, 1) and + 8 (e 2, 3), tokens 8 j + 2 t + (e & 1)
+    // features g (e 0, 1) and g + 8 (e 2, 3), tokens 2 t + (e & 1)
 #pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-      for (int j = 0; j < kNT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          red[warp][8 * j + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] = acc[i][j][e];
+    for (int e = 0; e < 4; ++e) red[warp][2 * t + (e & 1)][g + 8 * (e >> 1)] = acc[e];
     __syncthreads();
     for (int o = threadIdx.x; o < kTok * kFeat; o += 32 * kSmallWarps) {
       const int tok = o / kFeat, f = o - tok * kFeat;

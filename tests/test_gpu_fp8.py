@@ -206,6 +206,24 @@ def test_gemm_strides_weights_and_given_output(M, N, K):
         assert torch.all(buf[rest] == -7.0)
 
 
+@pytest.mark.parametrize("M,N", [(200, 1003), (600, 700), (300, 20013)])
+@pytest.mark.parametrize("out_dtype", TYPES)
+def test_gemm_columns_end_inside_a_unit_of_the_output_rows(M, N, out_dtype):
+    """Aligned output rows whose last column is not at a 16-byte boundary, with
+    every width of tile: the rest of the row stays."""
+    dg = _dg()
+    K = 130
+    rng = np.random.default_rng(N)
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K)
+    sa = sa * 2.0 ** -14
+    buf = torch.full((M, (N + 15) // 16 * 16), -7.0, dtype=out_dtype, device="cuda")
+    got = dg.fp8_gemm(a, sa, b, sb, out=buf[:, :N])
+    want, want_abs = ref.product(ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb))
+    _check(got, want, want_abs, K)
+    assert torch.all(buf[:, N:] == -7.0)
+
+
 @pytest.mark.parametrize("M", [1, 12, 200])
 def test_gemm_nan_stays_in_its_row_and_column(M):
     """A NaN scale makes exactly its row's (its 128 columns') results NaN; so
