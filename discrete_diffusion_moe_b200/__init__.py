@@ -132,6 +132,10 @@ def _load():
         "dg_router_probe": (I32, [P, I32, P, I32, P, P]),
         "dg_ar_step": (I32, [P, ctypes.POINTER(dg_kv), P, F, U64, P, P, P, P]),
         "dg_attention_static_scratch": (I32, [P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P]),
+        "dg_fp8_experts_bytes": (S, [cfgp]),
+        "dg_fp8_experts_scratch_bytes": (S, [P]),
+        "dg_fp8_experts_quantize": (I32, [P, P, S, P]),
+        "dg_fp8_experts_use": (I32, [P, P, P, S]),
         "dg_fp8_quantize": (I32, [P, I32, I64, I64, P, I32, I64, I64, P, I64, P, I64, P]),
         "dg_fp8_quantize_blocks": (I32, [P, I32, I64, I64, I64, I64, P, I64, P, P]),
         "dg_fp8_gemm": (I32, [P, I64, P, I64, P, I64, P, I64, I64, I64, P, P, I32, I64, P]),

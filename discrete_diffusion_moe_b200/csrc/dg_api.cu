@@ -140,6 +140,51 @@ WLayout weight_layout(const dg_model_config& c) {
   return w;
 }
 
+// 8-bit expert matrices of all layers: per layer the gate/up codes [E, 2 f, d]
+// and the down codes [E, d, f], then their scales per 128 x 128 block.
+struct Fp8LayerW {
+  size_t gu, dn, s_gu, s_dn;
+};
+struct Fp8WLayout {
+  std::vector<Fp8LayerW> layers;
+  size_t total;
+};
+int blocks128(int n) { return (n + 127) / 128; }
+
+Fp8WLayout fp8_weight_layout(const dg_model_config& c) {
+  Fp8WLayout w;
+  size_t off = 0;
+  auto take = [&](size_t n) { size_t o = off; off = align_up(off + n, 256); return o; };
+  const size_t E = c.n_experts, f = c.d_ff, d = c.d_model;
+  for (int l = 0; l < c.n_layers; ++l) {
+    Fp8LayerW L;
+    L.gu = take(E * 2 * f * d);
+    L.dn = take(E * d * f);
+    L.s_gu = take(E * blocks128(2 * c.d_ff) * blocks128(c.d_model) * 4);
+    L.s_dn = take(E * blocks128(c.d_model) * blocks128(c.d_ff) * 4);
+    w.layers.push_back(L);
+  }
+  w.total = off;
+  return w;
+}
+
+// Scratch of a context's 8-bit expert block for P slots (token, expert).
+struct Fp8Scratch {
+  size_t x, sx, y, h, sh, total;
+};
+Fp8Scratch fp8_scratch_layout(const dg_model_config& c, size_t P) {
+  Fp8Scratch s;
+  size_t off = 0;
+  auto take = [&](size_t n) { size_t o = off; off = align_up(off + n, 256); return o; };
+  s.x = take(P * c.d_model);
+  s.sx = take(P * blocks128(c.d_model) * 4);
+  s.y = take(P * 2 * c.d_ff * 2);
+  s.h = take(P * c.d_ff);
+  s.sh = take(P * blocks128(c.d_ff) * 4);
+  s.total = off;
+  return s;
+}
+
 constexpr int kMaxAttnSplits = 8;
 
 struct WsLayout {
@@ -557,11 +602,14 @@ struct dg_ctx {
   }
   dg_model_config cfg;
   const uint16_t* w;
+  const uint8_t* w8 = nullptr;  // 8-bit expert matrices in use (fp8_weight_layout), or null
+  uint8_t* ws8 = nullptr;       // their scratch (fp8_scratch_layout)
   uint8_t* ws;
   size_t ws_bytes;
   int batch_max;
   int num_sms;
   WLayout wl;
+  Fp8WLayout w8l;
   WsLayout L;
   template <class T>
   T* at(size_t off) const { return reinterpret_cast<T*>(ws + off); }
@@ -714,6 +762,49 @@ extern "C" dg_status dg_context_create_ex(const dg_model_config* cfg, const void
 }
 
 extern "C" void dg_context_destroy(dg_ctx* ctx) { delete ctx; }
+
+extern "C" size_t dg_fp8_experts_bytes(const dg_model_config* cfg) {
+  char why[256];
+  if (!cfg_ok(cfg, why, sizeof why)) { fail(DG_ERR_INVALID_ARG, "%s", why); return 0; }
+  return fp8_weight_layout(*cfg).total;
+}
+
+extern "C" size_t dg_fp8_experts_scratch_bytes(const dg_ctx* c) {
+  if (!c) { fail(DG_ERR_INVALID_ARG, "null context"); return 0; }
+  return fp8_scratch_layout(c->cfg, (size_t)c->L.P_alloc).total;
+}
+
+extern "C" dg_status dg_fp8_experts_quantize(const dg_ctx* c, void* d_experts, size_t bytes, void* stream) {
+  if (!c) return fail(DG_ERR_INVALID_ARG, "null context");
+  if (!d_experts || ((uintptr_t)d_experts & 255)) return fail(DG_ERR_INVALID_ARG, "experts must be non-null and 256-byte aligned");
+  const dg_model_config& m = c->cfg;
+  const Fp8WLayout w = fp8_weight_layout(m);
+  if (bytes < w.total) return fail(DG_ERR_INVALID_ARG, "experts buffer too small: %zu < %zu", bytes, w.total);
+  uint8_t* e = (uint8_t*)d_experts;
+  const int E = m.n_experts, f = m.d_ff, d = m.d_model;
+  for (int l = 0; l < m.n_layers; ++l) {
+    const LayerW& W = c->wl.layers[l];
+    const Fp8LayerW& W8 = w.layers[l];
+    DG_TRY(dg_fp8_quantize_blocks(c->wp(W.wgu), DG_BF16, d, E, 2 * f, d, e + W8.gu, d, (float*)(e + W8.s_gu), stream));
+    DG_TRY(dg_fp8_quantize_blocks(c->wp(W.wd), DG_BF16, f, E, d, f, e + W8.dn, f, (float*)(e + W8.s_dn), stream));
+  }
+  return DG_OK;
+}
+
+extern "C" dg_status dg_fp8_experts_use(dg_ctx* c, const void* d_experts, void* d_scratch, size_t scratch_bytes) {
+  if (!c) return fail(DG_ERR_INVALID_ARG, "null context");
+  if (d_experts) {
+    if (!d_scratch || ((uintptr_t)d_experts & 255) || ((uintptr_t)d_scratch & 255))
+      return fail(DG_ERR_INVALID_ARG, "experts and scratch must be non-null and 256-byte aligned");
+    const size_t need = fp8_scratch_layout(c->cfg, (size_t)c->L.P_alloc).total;
+    if (scratch_bytes < need) return fail(DG_ERR_WORKSPACE, "experts scratch too small: %zu < %zu", scratch_bytes, need);
+    c->w8l = fp8_weight_layout(c->cfg);
+  }
+  c->w8 = (const uint8_t*)d_experts;
+  c->ws8 = d_experts ? (uint8_t*)d_scratch : nullptr;
+  c->drop_graph();  // captured with the other expert path
+  return DG_OK;
+}
 
 // ---------------------------------------------------------------------------
 // Attention of one pass on the tensor cores: q packed [B][Hkv][nq][G][hd],
@@ -989,7 +1080,29 @@ static dg_status forward_layers(dg_ctx* c, const dg_kv* kv, int B, int nq, int L
       else return fail(DG_ERR_UNSUPPORTED, "router split count %d", ksr);
       CNT(c);
     }
-    if (pair && DG_MOE_FUSED) {
+    if (c->w8) {
+      // 8-bit experts: the gathered rows and the SwiGLU products are quantised per
+      // row and block of 128, the weights are read at one byte
+      const Fp8LayerW W8 = c->w8l.layers[l];
+      const Fp8Scratch s8 = fp8_scratch_layout(m, (size_t)L.P_alloc);
+      uint8_t *x8 = c->ws8 + s8.x, *h8 = c->ws8 + s8.h;
+      float *sx = (float*)(c->ws8 + s8.sx), *sh = (float*)(c->ws8 + s8.sh);
+      uint16_t* y8 = (uint16_t*)(c->ws8 + s8.y);
+      const int* off = c->at<int>(L.off);
+      {
+        ProfScope ps_(c, DG_PROF_EXPERT_GATE_UP, st);
+        DG_TRY(dg_fp8_quantize(c->at<uint16_t>(L.xperm), DG_BF16, d, P, nullptr, DG_ACT_NONE, P, d, x8, d, sx, P, st));
+        DG_TRY(dg_fp8_grouped_gemm(x8, d, sx, P, c->w8 + W8.gu, d, (const float*)(c->w8 + W8.s_gu), off, E, P, 2 * f, d,
+                                   nullptr, y8, DG_BF16, 2 * f, st));
+      }
+      {
+        ProfScope ps_(c, DG_PROF_EXPERT_DOWN, st);
+        DG_TRY(dg_fp8_quantize(y8, DG_BF16, 2 * f, P, nullptr, DG_ACT_SWIGLU_INTERLEAVED, P, f, h8, f, sh, P, st));
+        DG_TRY(dg_fp8_grouped_gemm(h8, f, sh, P, c->w8 + W8.dn, f, (const float*)(c->w8 + W8.s_dn), off, E, P, d, f,
+                                   c->at<float>(L.wperm), c->at<float>(L.yperm), DG_F32, d, st));
+      }
+      c->n_launch += 4;
+    } else if (pair && DG_MOE_FUSED) {
       // gate/up + SwiGLU and down in one launch
       ProfScope ps_(c, DG_PROF_EXPERT_GATE_UP, st);
       CUtensorMap ta1, ta2;

@@ -164,6 +164,26 @@ class Model:
         except Exception:
             pass
 
+    def quantize_experts(self, stream=None) -> torch.Tensor:
+        """The model's expert matrices in 8 bits (dg_fp8_experts_quantize), for
+        use_fp8_experts of this model or of one that shares its weights."""
+        n = lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg))
+        experts = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
+        check(lib.dg_fp8_experts_quantize(self.ctx, _ptr(experts), n, _stream(stream)))
+        return experts
+
+    def use_fp8_experts(self, experts: torch.Tensor = None):
+        """Run the expert blocks on 8-bit matrices (dg_fp8_experts_use);
+        None goes back to bf16."""
+        scratch, n = None, 0
+        if experts is not None:
+            if experts.dtype != torch.uint8 or experts.numel() < lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg)):
+                raise ValueError("experts: a uint8 tensor from quantize_experts of the same configuration is needed")
+            n = lib.dg_fp8_experts_scratch_bytes(self.ctx)
+            scratch = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
+        check(lib.dg_fp8_experts_use(self.ctx, _ptr(experts), _ptr(scratch), n))
+        self.experts8, self.scratch8 = experts, scratch   # keeps them alive
+
     def encode(self, kv: KVCache, tokens: torch.Tensor, stream=None):
         assert tokens.dtype == torch.int32 and tokens.is_contiguous()
         check(lib.dg_encode_context(self.ctx, ctypes.byref(kv.s), _ptr(tokens), tokens.shape[1],

@@ -434,6 +434,32 @@ dg_status dg_fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_
                               int64_t groups, int64_t M, int64_t N, int64_t K, const float* d_row_weight, void* d_out,
                               int32_t out_dtype, int64_t ldo, void* stream);
 
+/* ---- 8-bit experts of a context -------------------------------------------
+   A context's expert block on 8-bit matrices: after the routing the gathered
+   rows are quantised (dg_fp8_quantize), multiplied with the gate/up matrices
+   (dg_fp8_grouped_gemm, bf16 out), put through SwiGLU and quantised again, and
+   multiplied with the down matrices and the routing weights (fp32 out).
+   Router, attention, projections and LM head stay bf16.  Every call that runs
+   the layers uses them (encode, rounds, graphs, blocks, autoregressive steps);
+   results differ from the bf16 experts' by the two roundings to e4m3.
+
+   dg_fp8_experts_bytes: bytes of the expert matrices of all layers (codes and
+   scales; about half of the bf16 ones), 0 on a bad configuration.  Layout, each
+   part 256-byte aligned, per layer: gate/up codes [E, 2 d_ff, d_model] (gate row
+   j at 2j, up row at 2j + 1), down codes [E, d_model, d_ff], gate/up scales
+   [E, ceil(2 d_ff / 128), ceil(d_model / 128)], down scales
+   [E, ceil(d_model / 128), ceil(d_ff / 128)].
+   dg_fp8_experts_quantize fills such a buffer from the context's weights
+   (asynchronous on `stream`); contexts of the same weights may share it.
+   dg_fp8_experts_use switches the context to it (NULL: back to bf16) with a
+   scratch buffer of dg_fp8_experts_scratch_bytes(ctx) bytes of its own, like
+   the workspace: calls on one context must not overlap on the GPU.  Host-side
+   only; it drops the context's captured graph. */
+size_t dg_fp8_experts_bytes(const dg_model_config* cfg);
+size_t dg_fp8_experts_scratch_bytes(const dg_ctx* ctx);
+dg_status dg_fp8_experts_quantize(const dg_ctx* ctx, void* d_experts, size_t bytes, void* stream);
+dg_status dg_fp8_experts_use(dg_ctx* ctx, const void* d_experts, void* d_scratch, size_t scratch_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -84,3 +84,16 @@ def test_tensors_on_the_cpu_are_refused():
                  lambda: dg.fp8_grouped_gemm(e, torch.ones(1, 4), e[None], torch.ones(1, 1, 1), torch.zeros(2).int())):
         with pytest.raises(ValueError):
             call()
+
+
+def test_expert_buffer_sizes_and_null_contexts():
+    import ctypes
+    import discrete_diffusion_moe_b200 as dg
+    cfg = dg.model_config(30, 2816, 16, 8, 176, 128, 8, 704, 262144)
+    codes, scales = 128 * 3 * 704 * 2816, 128 * 4 * (11 * 22 + 22 * 6)
+    assert dg.lib.dg_fp8_experts_bytes(ctypes.byref(cfg)) == 30 * (codes + scales)   # parts are multiples of 256 here
+    bad = dg.model_config(1, 100, 1, 1, 32, 4, 2, 64, 4096)
+    assert dg.lib.dg_fp8_experts_bytes(ctypes.byref(bad)) == 0
+    assert dg.lib.dg_fp8_experts_scratch_bytes(None) == 0
+    assert dg.lib.dg_fp8_experts_quantize(None, A, 1 << 30, None) == dg.DG_ERR_INVALID_ARG
+    assert dg.lib.dg_fp8_experts_use(None, None, None, 0) == dg.DG_ERR_INVALID_ARG
