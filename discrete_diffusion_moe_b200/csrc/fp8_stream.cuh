@@ -208,9 +208,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     for (int u = first; u < U; u += stride) {
       const Fp8Job j = job(u);
       const int n_ld = (j.row1 - j.row0 + 31) / 32;  // 32-token parts
-      float acc[kTok];
+      float acc[kTok], rw[kTok / 32];  // rw: the row weights of tokens lane, lane + 32, ..
 #pragma unroll
       for (int i = 0; i < kTok; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTok / 32; ++i) rw[i] = p.row_w ? __ldg(p.row_w + min(j.row0 + 32 * i + lane, j.row1 - 1)) : 1.f;
 #pragma unroll 1
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t slot = batch % S::kScaleSlots, b = it % S::kBufs;
@@ -253,13 +255,15 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         continue;
       }
       const bool bad = ld_shared_flag(dead) != 0;  // a wait ran out: what was added is not the product
-      TO* const o = static_cast<TO*>(p.out) + (long long)j.row0 * p.ldo + n;
+      TO* o = static_cast<TO*>(p.out) + (long long)j.row0 * p.ldo + n;
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (i < rows && n < p.N) {
-          float v = bad ? __uint_as_float(0x7fffffffu) : acc[i];
-          if (p.row_w) v *= __ldg(p.row_w + j.row0 + i);
-          store_out(o + (long long)i * p.ldo, v);
+      for (int c = 0; c < kTok / 32; ++c) {
+        if (c < n_ld) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i, o += p.ldo) {
+            const float w = __shfl_sync(0xffffffffu, rw[c], i);
+            if (c * 32 + i < rows && n < p.N) store_out(o, bad ? __uint_as_float(0x7fffffffu) : acc[c * 32 + i] * w);
+          }
         }
       }
     }
