@@ -306,10 +306,23 @@ __device__ __forceinline__ void store_turned(uint8_t* turn, const CUtensorMap* m
           *reinterpret_cast<uint4*>(out + r * ldo + c0 + u * kUnit) =
               *reinterpret_cast<const uint4*>(buf + r * 128 + ((u ^ (r & 7)) * 16));
       } else {
-        for (int r = 0; r < rows; ++r)
-        for (int c = lane; c < n; c += 32)
-          out[r * ldo + c0 + c] =
-              *reinterpret_cast<const TO*>(buf + r * 128 + (((c / kUnit) ^ (r & 7)) * 16) + (c % kUnit) * sizeof(TO));
+        // unaligned or cut rows: element by element, eight rows in flight
+        constexpr int kEach = (kPass + 31) / 32;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+          TO v[8][kEach];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              const int r = r0 + k, c = (lane + 32 * e) % kPass;
+              v[k][e] = *reinterpret_cast<const TO*>(buf + r * 128 + (((c / kUnit) ^ (r & 7)) * 16) + (c % kUnit) * sizeof(TO));
+            }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+              if (r0 + k < rows && lane + 32 * e < n) out[(r0 + k) * ldo + c0 + lane + 32 * e] = v[k][e];
+        }
       }
       if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // keeps the count of passes
       __syncwarp();
