@@ -221,7 +221,7 @@ extern "C" dg_status dg_fp8_quantize(const void* d_x, int32_t dtype, int64_t ldx
   p.x = d_x; p.ldx = ldx; p.index = d_index; p.x_rows = x_rows;
   p.q = d_q; p.ldq = ldq; p.scale = d_scale; p.lds = lds;
   p.rows = (int)rows; p.K = (int)cols; p.KB = (int)ceil_div(cols, kFp8Block);
-  if (ceil_div((long long)p.rows * p.KB, (long long)kQuantThreads / 32 * 2 * kQuantTasks) > kMaxDim)
+  if ((long long)p.rows * p.KB > kMaxDim - 64)  // the kernel counts blocks in 32 bits
     return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: too many blocks");
   const bool vec = cols % 8 == 0 && aligned(d_x, 16) && (ldx * (long long)sz) % 16 == 0;
   cudaStream_t st = (cudaStream_t)stream;

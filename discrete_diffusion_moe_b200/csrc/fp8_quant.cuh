@@ -75,14 +75,18 @@ __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g,
 struct BlockScale {
   float scale, inv;
 };
-// amax_bits: the largest bit pattern of |x| of the block; patterns from
-// infinity up (infinities and NaNs) compare above every finite one
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
-  if (amax_bits >= 0x7f800000u) return {__uint_as_float(0x7fffffffu), 0.f};
-  const float a = fmaxf(__uint_as_float(amax_bits), kFp8AmaxMin);
-  return {__fdiv_rn(a, kE4m3Max), __fdiv_rn(kE4m3Max, a)};
-}
+// Bit patterns of magnitudes compare like the magnitudes, infinities and NaNs
+// above all others.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// m: the block's largest magnitude (NaN where it holds one).  The quotient by the
+// constant 448 is the product with its reciprocal corrected by the remainder
+// (Markstein, 1990): rounded correctly, since every term is a normal number for m
+// of 2^-100 and more.
+__device__ __forceinline__ BlockScale block_scale(float m) {
+  if (!(m <= 3.4028234663852886e38f)) return {__uint_as_float(0x7fffffffu), 0.f};
+  const float a = fmaxf(m, kFp8AmaxMin), r = 1.0f / kE4m3Max, q = a * r;
+  return {fmaf(fmaf(-q, kE4m3Max, a), r, q), __fdiv_rn(kE4m3Max, a)};
+}
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -105,8 +109,9 @@ struct QuantRowsParams {
 // Half a warp takes one (row, block of 128 columns): eight elements per lane, so
 // a row's block is one 256-byte load of bf16 and the maximum takes four
 // shuffles.  A warp takes 2 * kQuantTasks consecutive tasks and issues all
-// their loads first: the kernel is latency-bound otherwise (one load in flight
-// per lane reached about half the bandwidth).  kVec: 16-byte loads and 8-byte
+// their loads first.  With SwiGLU the instructions count as much as the bytes
+// (23 M results of 92 MB: 37 instructions a result kept the schedulers at 80 %),
+// so a task's place takes one division per four tasks.  kVec: 16-byte loads and 8-byte
 // stores (every row of x 16-byte aligned and K a multiple of 8); otherwise lane
 // l takes elements l, l + 16, ... one by one.
 constexpr int kQuantTasks = 4;
@@ -117,9 +122,11 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantRo
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, l = lane & 15;
-  const long long warp = (long long)blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
-  const long long tasks = (long long)p.rows * p.KB;
-  const long long first = warp * (2 * kQuantTasks) + (lane >> 4);
+  // tasks below 2^31 (the host's check); one division, the later tasks by steps
+  const unsigned warp = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
+  const unsigned tasks = (unsigned)p.rows * (unsigned)p.KB;
+  const unsigned first = warp * (2 * kQuantTasks) + (lane >> 4);
+  int next_row = (int)(first / (unsigned)p.KB), next_kb = (int)(first - (unsigned)next_row * (unsigned)p.KB);
   constexpr int kIn = ACT == kActNone ? 1 : 2;
   const T* const x = static_cast<const T*>(p.x);
 
@@ -128,9 +135,9 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantRo
   float v[kQuantTasks][8];
 #pragma unroll
   for (int u = 0; u < kQuantTasks; ++u) {
-    const long long t = first + 2 * u;
-    row[u] = t < tasks ? (int)(t / p.KB) : -1;
-    kb[u] = t < tasks ? (int)(t - (long long)row[u] * p.KB) : 0;
+    row[u] = first + 2 * u < tasks ? next_row : -1;
+    kb[u] = next_kb;
+    for (next_kb += 2; next_kb >= p.KB; next_kb -= p.KB) ++next_row;
     long long src = row[u];
     if (p.index && row[u] >= 0) {
       src = __ldg(p.index + row[u]);
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantRo
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (row[u] < 0) continue;
-    const BlockScale s = block_scale(m);
+    const BlockScale s = block_scale(__uint_as_float(m));
     uint8_t* const qr = p.q + (long long)row[u] * p.ldq + kb[u] * kFp8Block;
     uint32_t lo = 0u, hi = 0u;
     if (s.inv != 0.f) {  // codes 0 where the scale is NaN
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const QuantBlocksPara
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, s_max[i]);
-  const BlockScale s = block_scale(m);
+  const BlockScale s = block_scale(__uint_as_float(m));
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int n = nb * kFp8Block + u * 16 + r0;
