@@ -16,7 +16,7 @@ using namespace dg;
 
 namespace {
 
-constexpr long long kMaxDim = 2147483647ll;
+constexpr long long kMaxDim = 2147483647ll - 4096;  // tile coordinates stay within 32 bits
 
 size_t dtype_bytes(int dt) { return dt == DG_F32 ? 4 : 2; }
 bool dtype_ok(int dt) { return dt == DG_BF16 || dt == DG_F16 || dt == DG_F32; }
@@ -168,7 +168,7 @@ dg_status check_product(const char* who, const uint8_t* a, int64_t lda, const fl
     return fail(DG_ERR_INVALID_ARG, "%s: sizes %lld x %lld x %lld", who, (long long)M, (long long)N, (long long)K);
   if (!dtype_ok(out_dtype)) return fail(DG_ERR_INVALID_ARG, "%s: output type %d", who, (int)out_dtype);
   if (G < 1 || G > kFp8MaxGroups) return fail(DG_ERR_INVALID_ARG, "%s: %lld groups (1..%d)", who, (long long)G, kFp8MaxGroups);
-  if (G * N > kMaxDim) return fail(DG_ERR_INVALID_ARG, "%s: groups x N exceeds 2^31 - 1", who);
+  if (G * N > kMaxDim) return fail(DG_ERR_INVALID_ARG, "%s: groups x N exceeds 2^31 - 4097", who);
   if (lda < K || lda % 16 || ldb < K || ldb % 16)
     return fail(DG_ERR_INVALID_ARG, "%s: row pitches %lld, %lld of the codes (multiples of 16, at least K = %lld)", who,
                 (long long)lda, (long long)ldb, (long long)K);
@@ -221,7 +221,7 @@ extern "C" dg_status dg_fp8_quantize(const void* d_x, int32_t dtype, int64_t ldx
   p.x = d_x; p.ldx = ldx; p.index = d_index; p.x_rows = x_rows;
   p.q = d_q; p.ldq = ldq; p.scale = d_scale; p.lds = lds;
   p.rows = (int)rows; p.K = (int)cols; p.KB = (int)ceil_div(cols, kFp8Block);
-  if ((long long)p.rows * p.KB > kMaxDim - 64)  // the kernel counts blocks in 32 bits
+  if ((long long)p.rows * p.KB > kMaxDim)  // the kernel counts blocks in 32 bits
     return fail(DG_ERR_INVALID_ARG, "dg_fp8_quantize: too many blocks");
   const bool vec = cols % 8 == 0 && aligned(d_x, 16) && (ldx * (long long)sz) % 16 == 0;
   cudaStream_t st = (cudaStream_t)stream;

@@ -225,7 +225,7 @@ __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Table
 template <int kW>
 struct Fp8Shape {
   static constexpr int kBufs = kW >= 256 ? 2 : 4;  // tensor-memory buffers of kW columns
-  static constexpr int kStages = kW >= 256 ? 4 : (kW >= 128 ? 5 : 6);
+  static constexpr int kStages = kW >= 256 ? 4 : 5;
   static constexpr int kStageA = 128 * 128, kStageB = (kW / 2) * 128;
   static constexpr int kTurn = kFp8EpiWarps * 8192;  // two buffers of 32 rows x 128 bytes per warp
   static constexpr int kCols = kW / 2;               // columns of an epilogue warp
@@ -376,7 +376,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     for (int i = 0; i < 2; ++i) tma_prefetch_desc(&maps.b[i]);
   }
   grid_dep_wait();
-  grid_dep_launch();
   int m_tiles = (p.M + 255) / 256;
   if (p.off && warp == 4) fp8_tables<256>(p, tabs, lane);
   __syncthreads();
@@ -388,6 +387,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before the tensor memory is held: the next kernel's CTAs may want it too
   const uint32_t tmem_base = *tmem_slot;
   if (p.off) m_tiles = tabs.first[p.G];
   const int U = m_tiles * n_tiles;

@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   const uint32_t tmem_base = *tmem_slot;
   const int f_tiles = (p.N + 127) / 128;
   const int chunks = p.off ? tabs.first[p.G] : (p.M + kTok - 1) / kTok;
-  const int U = f_tiles * chunks;
+  // a cluster has one unit, whatever the offsets say
+  const int U = splits > 1 ? min(f_tiles * chunks, stride) : f_tiles * chunks;
   // unit u: a group's feature tiles one after the other, the chunks of a tile side by side
   auto job = [&](int u) { return fp8_job<kTok>(p, tabs, u, chunks, f_tiles, 128); };
 

@@ -117,6 +117,26 @@ def test_quantize_swiglu(rows, K, act, dtype):
     assert np.all(np.abs(got - v) <= bound), float((np.abs(got - v) / bound).max())
 
 
+@pytest.mark.parametrize("act", ["swiglu", "swiglu_interleaved"])
+def test_quantize_swiglu_special_values(act):
+    """Gates of either infinity and far from zero, NaN gates and values: the
+    blocks that hold no finite result are NaN, the others as the formula says."""
+    dg = _dg()
+    K = 130
+    g, u = torch.ones(8, K), torch.full((8, K), 2.0)
+    g[0, 3], g[1, 129], g[2, 0] = float("nan"), float("inf"), -float("inf")
+    u[3, 5], u[4, 128] = float("nan"), -float("inf")
+    g[5], g[6], g[7] = -200.0, 200.0, 0.0
+    x = torch.stack((g, u), -1).view(8, 2 * K) if act != "swiglu" else torch.cat((g, u), 1)
+    q, s = dg.fp8_quantize(x.cuda(), act=act)
+    bad = torch.zeros(2, 8, dtype=torch.bool)
+    bad[0, 0] = bad[1, 1] = bad[0, 2] = bad[0, 3] = bad[1, 4] = True
+    assert torch.equal(torch.isnan(s).cpu(), bad)
+    v = ref.dequantize_rows(q, s)
+    assert np.all(v[5] == 0.0) and np.all(v[7] == 0.0)
+    assert np.all(np.abs(v[6] - 400.0) <= 400.0 * 2.0 ** -20)   # the block's largest value takes the largest code
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("G,N,K", [(None, 1, 1), (None, 128, 128), (None, 130, 257), (2, 64, 704), (3, 129, 99), (1, 300, 1024)])
 def test_quantize_blocks(G, N, K, dtype):
@@ -300,6 +320,24 @@ def test_grouped_gemm_offsets_outside_are_held_inside():
     av, bv = ref.dequantize_rows(a, sa), ref.dequantize_blocks(b, sb)
     for g, (lo, hi) in enumerate([(0, 4), (4, 20), (20, 30)]):
         _check(out[lo:hi], *ref.product(av[lo:hi], bv[g]), K)
+
+
+def test_grouped_gemm_decreasing_offsets_stay_inside():
+    """Offsets that decrease are the caller's mistake: whatever is computed, rows
+    of no group and the memory around the output stay."""
+    dg = _dg()
+    rng = np.random.default_rng(6)
+    N, K, M = 160, 256, 200
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K, G=4)
+    buf = torch.full((M + 8, N), -3.0, device="cuda")
+    for off in ([0, 100, 50, 120, 90], [180, 20, 5, 0, 0], [7, 7, 3, 9, 2]):
+        buf.fill_(-3.0)
+        dg.fp8_grouped_gemm(a, sa, b, sb, torch.tensor(off, dtype=torch.int32, device="cuda"), out=buf[4:4 + M])
+        inside = torch.zeros(M + 8, dtype=torch.bool)
+        for lo, hi in zip(off, off[1:]):
+            inside[4 + lo:4 + max(lo, hi)] = True
+        assert torch.all(buf.cpu()[~inside] == -3.0)
 
 
 def test_no_rows():
