@@ -115,6 +115,12 @@ __device__ __forceinline__ void wait_or_die(uint32_t bar, uint32_t parity, uint3
   }
   __syncwarp();
 }
+// The same for what has to end before the CTA may leave (copies into its memory,
+// MMAs that read it): a failed wait elsewhere does not cut it short.
+__device__ __forceinline__ void wait_to_leave(uint32_t bar, uint32_t parity) {
+  mbar_wait(bar, parity, nullptr);
+  __syncwarp();
+}
 // 32 lanes x 32 consecutive fp32 columns of tensor memory; the registers are
 // undefined until tmem_wait32 on them
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
@@ -225,14 +231,20 @@ __device__ __forceinline__ Fp8Job fp8_job(const Fp8GemmParams& p, const Fp8Table
 template <int kW>
 struct Fp8Shape {
   static constexpr int kBufs = kW >= 256 ? 2 : 4;  // tensor-memory buffers of kW columns
-  static constexpr int kStages = kW >= 256 ? 4 : 5;
+  // Even, so that an MMA warp, which takes every second block, comes back to the same
+  // stages and has itself seen each phase of their barriers.  A wait tells only a
+  // phase from the one before it: with an odd number a warp could pass on the
+  // phase two back while the other warp's copy into the stage was still under way.
+  static constexpr int kStages = kW >= 256 ? 4 : 6;
+  static_assert(kStages % 2 == 0 && kBufs % 2 == 0, "two MMA warps in turn");
   static constexpr int kStageA = 128 * 128, kStageB = (kW / 2) * 128;
   static constexpr int kTurn = kFp8EpiWarps * 8192;  // two buffers of 32 rows x 128 bytes per warp
   static constexpr int kCols = kW / 2;               // columns of an epilogue warp
   // row and weight scales of four blocks per slot: [128][4], and [4] for either half of the columns
-  static constexpr int kScaleSlots = 4, kScaleSlot = 4 * 128 + 4 * 2;
+  static constexpr int kScaleSlots = kW >= 256 ? 4 : 2, kScaleSlot = 4 * 128 + 4 * 2;
   static constexpr int kBars = 2 * kStages + kBufs + 2 * kScaleSlots + 1;
   static constexpr int kSmem = 1024 + kStages * (kStageA + kStageB) + kTurn + kScaleSlots * kScaleSlot * 4 + kBars * 8 + 16;
+  static_assert(kSmem + 13 * 1024 <= 227 * 1024, "shared memory, with the tables of the groups");
 };
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
@@ -431,7 +443,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // the leader's full barriers count both CTAs' bytes: wait until all have landed
       if (rank == 0) {
         const uint32_t first = issued > (uint32_t)S::kStages ? issued - S::kStages : 0;
-        for (uint32_t q = first; q < issued; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
+        for (uint32_t q = first; q < issued; ++q) wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1);
       }
     } else if (warp == 1 || warp == 3) {
       if (rank == 0) {
@@ -470,7 +482,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           kb -= p.KB;
         }
         if (elect_one()) umma_commit_pair(drain);
-        wait_or_die(drain, 0, dead);
+        wait_to_leave(drain, 0);
+        // and the other CTA's last arrivals have come: none is on its way to a CTA that left
+#pragma unroll
+        for (int i = 0; i < S::kBufs / 2; ++i) {
+          wait_or_die(acc_empty + b * 8u, b_phase, dead);
+          b = (b + 2) % S::kBufs;
+          if (b == m) b_phase ^= 1;
+        }
       }
     } else if (warp == 2) {
       // ---------------- scales (both CTAs) ----------------

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         __syncwarp();
       }
     }
-    for (uint32_t q = it > (uint32_t)S::kStages ? it - S::kStages : 0; q < it; ++q) wait_or_die(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead);
+    for (uint32_t q = it > (uint32_t)S::kStages ? it - S::kStages : 0; q < it; ++q) wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1);
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     uint32_t it = 0;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       }
     }
     if (elect_one()) umma_commit(drain);
-    wait_or_die(drain, 0, dead);
+    wait_to_leave(drain, 0);
   } else if (warp == 2) {
     // ---------------- scales: four blocks per slot ----------------
     uint32_t batch = 0;

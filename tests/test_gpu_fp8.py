@@ -358,6 +358,76 @@ def test_no_rows():
     assert torch.all(out == 2.0)
 
 
+def test_offsets_beyond_32_bits():
+    """An output and a set of weights of more than 2^32 bytes: their last rows."""
+    dg = _dg()
+    rng = np.random.default_rng(12)
+    M, N, K = 8200, 262144, 48
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K)
+    got = dg.fp8_gemm(a, sa, b, sb)
+    assert got.numel() * 2 > 2 ** 32
+    want, want_abs = ref.product(ref.dequantize_rows(a, sa)[-9:], ref.dequantize_blocks(b, sb))
+    _check(got[-9:], want, want_abs, K)
+    del got, b
+
+    G, N, K = 512, 4096, 2064   # 4.3 GB of codes; the rows all belong to the last matrices
+    codes = torch.randint(0, 112, (G, N, K), device="cuda", dtype=torch.uint8)
+    sb = torch.rand(G, ref.blocks(N), ref.blocks(K), device="cuda")
+    assert codes.numel() > 2 ** 32
+    for sizes in ((1, 2), (40, 30), (300, 700)):     # every kernel
+        M = sum(sizes)
+        a, sa = ref.random_operand(rng, M, K)
+        off = torch.full((G + 1,), M, dtype=torch.int32, device="cuda")
+        off[:G - 1], off[G - 1] = 0, sizes[0]
+        out = dg.fp8_grouped_gemm(a, sa, codes.view(torch.float8_e4m3fn), sb, off)
+        av, row = ref.dequantize_rows(a, sa), 0
+        for g, n in zip((G - 2, G - 1), sizes):
+            want = ref.product(av[row:row + n], ref.dequantize_blocks(codes[g].view(torch.float8_e4m3fn), sb[g]))
+            _check(out[row:row + n], *want, K)
+            row += n
+
+
+def _in_range(got, want, want_abs, K):
+    """The results without those outside got's type.  A value is rounded to an infinity from
+    half a step above the largest finite one on (fp16: 65504 + 16); within the bound's
+    distance of that point both are right."""
+    if got.dtype != torch.float16:
+        return got, want, want_abs
+    edge, bound = 65520.0, ref.product_bound(want, want_abs, K, torch.float32)
+    out = got.double().cpu().numpy()
+    over = np.abs(want) - bound >= edge
+    assert np.all(np.isinf(out[over]) & (np.sign(out[over]) == np.sign(want[over])))
+    assert np.all(np.isfinite(out[np.abs(want) + bound < edge]))
+    keep = np.isfinite(out)
+    return got[torch.from_numpy(keep).cuda()], want[keep], want_abs[keep]
+
+
+@pytest.mark.parametrize("N,K,out", [(40, 3054, torch.bfloat16), (24, 4096, torch.float32), (128, 2816, torch.bfloat16),
+                                     (120, 1000, torch.float16)])
+def test_few_columns_many_groups(N, K, out):
+    """One tile of columns per group and many ragged tiles of rows: units follow one
+    another quickly, and copies of far weights land out of order.  The same call again and
+    again gives the same bits."""
+    dg = _dg()
+    rng = np.random.default_rng(N)
+    sizes = [0 if g == 17 else int(rng.integers(130, 520)) for g in range(57)]
+    M = sum(sizes)
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)).cuda()
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K, G=len(sizes))
+    first = dg.fp8_grouped_gemm(a, sa, b, sb, off, out_dtype=out)
+    av, row = ref.dequantize_rows(a, sa), 0
+    for g, n in enumerate(sizes):
+        if n:
+            want, want_abs = ref.product(av[row:row + n], ref.dequantize_blocks(b[g], sb[g]))
+            _check(*_in_range(first[row:row + n], want, want_abs, K), K)
+        row += n
+    for _ in range(50):
+        again = [dg.fp8_grouped_gemm(a, sa, b, sb, off, out_dtype=out) for _ in range(8)]
+        assert all(torch.equal(first, x) for x in again)
+
+
 # ---- as they are used together ----------------------------------------------------------
 
 def _expert_block(dg, x, index, off, w1, w2, row_weight):
