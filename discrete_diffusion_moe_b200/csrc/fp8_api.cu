@@ -129,25 +129,34 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
   return DG_OK;
 }
 
-// Which kernel, by rows and columns (times of K = 2816, bf16 out, in us):
+// Which kernel, by rows and columns (us, K = 2816, bf16 out, where not said otherwise):
 //   at most 8 rows and two waves of its CTAs: mma.sync, where the set-up counts
-//     (one token, 5632 features: 6.3, streaming 9.4; 262144 features: 186, 111);
-//   at most 80 rows a group on average: the streaming kernel (1408 features, 128
-//     experts, 8192 rows: 130, pairs 154; 16384 rows: 223, 171);
-//   else CTA pairs, with the widest tile that still gives about every pair work
-//     (narrower tiles read A more often: 256 rows of 5632 features with 128
-//     columns a tile 13.5, with 64 14.9).
-constexpr int kStreamRows = 80;
+//     (one token, 5632 features: 6.6, streaming 9.7; 262144 features: 132, 108);
+//   at most kStreamRows rows, or kStreamGroupRows a group on average: the streaming
+//     kernel, which reads the weights once for 64 rows (262144 features: 64 rows
+//     127, pairs 212, 80 rows 225, 216; 1408 features of 128 experts: 8192 rows
+//     114, pairs 151, 12288 rows 159, 156);
+//     but from 33 rows on pairs if one wave of them does it and keeps more than half
+//     of them busy (5632 features, 64 rows: pairs 12.5, streaming 14.2; K = 704: 7.2,
+//     11.7; 2816 features, a smaller part of a wave: 11.9, 10.9);
+//   else CTA pairs, with tiles of 128 columns instead of 256 if that needs fewer than 5/3
+//     as many waves, the ratio of what a wave takes (256 rows of 5632 features: 13.2, 17.5;
+//     1024 rows: 27.6, 30.9; 8192 rows: 156, 138; 40000 rows of 128 features: 31.5, 40.1).
+// For groups the row tiles are an estimate: the offsets are on the device.
+constexpr int kStreamRows = 64, kStreamGroupRows = 80, kPairRows = 32;
 
 template <class TO>
 dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
   const int sms = device_sms(), pairs = sms / 2;
   const long long groups = p.off ? std::min(p.G, p.M) : 1;  // that may have rows
   if (p.M <= kSmallRows && groups * ceil_div(p.N, 16) <= 2ll * kSmallCtas * sms) return launch_small<TO>(p, st);
-  if (p.M <= kStreamRows * groups) return launch_stream<64, TO>(p, sms, st);
-  const long long tiles = p.off ? std::max<long long>(groups, p.M / 256) : ceil_div(p.M, 256);
-  if (tiles * ceil_div(p.N, 256) >= pairs) return launch_pair<256, TO>(p, pairs, st);
-  return launch_pair<128, TO>(p, pairs, st);
+  const long long tiles = p.off ? std::max<long long>(groups, groups / 2 + p.M / 256) : ceil_div(p.M, 256);
+  const long long units128 = tiles * ceil_div(p.N, 128), units256 = tiles * ceil_div(p.N, 256);
+  const bool one_wave = units128 <= pairs && 2 * units128 > pairs;
+  if (p.M <= (p.off ? kStreamGroupRows : kStreamRows) * groups && !(p.M > kPairRows * groups && one_wave))
+    return launch_stream<64, TO>(p, sms, st);
+  if (3 * ceil_div(units128, pairs) < 5 * ceil_div(units256, pairs)) return launch_pair<128, TO>(p, pairs, st);
+  return launch_pair<256, TO>(p, pairs, st);
 }
 
 dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, cudaStream_t st) {

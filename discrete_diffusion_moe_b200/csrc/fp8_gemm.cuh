@@ -16,12 +16,13 @@
 // add them in registers, while the tensor cores work on the next block in
 // another buffer.  fp32 throughout; one rounding at the store.
 //
-// kW = 256 where there is enough work: shared memory is what bounds the kernel.
-// Per block a CTA's tensor cores read 16 KB of A and 128 bytes of each B row, and
-// 32 KB are written by the copies, at 128 bytes a cycle; with N = 128 A is read
-// twice, and the MMAs alone keep shared memory busy (measured: 950 cycles per
-// block of 256 columns, every barrier answering after 100 cycles or more, where
-// N = 256 leaves a third of it free).
+// What bounds it, in cycles per block of 256 x 256 (the parts timed alone): copies 486,
+// MMAs 600, copies and MMAs together 790, since both use the shared memory, all with
+// the epilogue 1030.  The last step is the chain MMA - commit - take out - release -
+// MMA through two buffers of 256 columns, which fill the tensor memory.  8192 x 5632 x
+// 2816 into bf16: 138 us with 1.9 PFLOP/s; under a steady load of such products the
+// 1000 W limit takes the clock to 1.64 GHz (158 us).  With kW = 128 rows are read twice as
+// often, but there are four buffers and finer units, for small or ragged work.
 //
 // Each CTA of a pair copies its own 128 rows of A and half of the columns of B
 // (32 KB a stage at 256 columns), so a pair reads 512 rows per block.  Copies of
@@ -53,16 +54,16 @@ constexpr int kFp8MaxGroups = 1024;
 constexpr int kFp8EpiWarps = 8;
 // Warpgroup 0: a copying warp, two MMA warps, a scale warp; warpgroups 1 and 2:
 // the epilogue.  384 threads x 168 registers at launch; warpgroup 0 gives back what
-// the epilogue takes.  Nothing may spill: with nearly all of the SM's memory used
-// as shared memory a spilled register comes back from L2 (measured: 400 cycles a
-// part, half of the kernel's time).
+// the epilogue takes.  Spills count: with nearly all of the SM's memory used as
+// shared memory a spilled register comes back from L2, and several of them in the
+// loop over blocks doubled the kernel's time (one is left at kW = 256).
 constexpr int kFp8Threads = 128 + 32 * kFp8EpiWarps;
 constexpr int kFp8RegsCopy = 72, kFp8RegsEpi = 216;
 static_assert(128 * kFp8RegsCopy + 32 * kFp8EpiWarps * kFp8RegsEpi <= kFp8Threads * 168, "register split");
 
 // One lane of a converged warp.  The copies and MMAs take their descriptors from
 // uniform registers; issued from a branch on the lane number the compiler moves
-// them there one instruction at a time, which measured 120 cycles each.
+// them there one instruction at a time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -148,8 +149,8 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
 }
 // Arrive on a pair peer's (or this CTA's) mbarrier at the default scope.  What it
 // orders are tensor-memory reads, by the tcgen05 fence before it; a release at
-// cluster scope would add a memory barrier to every block of every warp, which
-// measured 2900 cycles per block in place of about 600.
+// cluster scope would add a memory barrier to every block of every warp (8192 x
+// 5632 x 2816 took 350 us with it and 205 without).
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // ---------------- scales (both CTAs) ----------------
       // Asynchronous copies of four blocks' scales per slot, up to four slots ahead: a
       // load queues behind the copies of every stage, and waiting for one slot before
-      // asking for the next set the pace of the whole kernel (950 cycles per block).
+      // asking for the next set the pace of the whole kernel.
       uint32_t slot = 0, phase = 1;
       for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
         const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);

@@ -15,7 +15,7 @@
 // per block.  The eight warps of a CTA share its 16 features and take every
 // eighth block of K each.  One block per warp is in flight, and 48 registers let
 // five CTAs share an SM: with three blocks in flight and two CTAs 5632 features
-// of one token took 7.7 us (two waves), so 6.3; 8 experts 14.0, so 10.4.  The
+// of one token took 7.7 us (two waves), so 6.6; 8 experts 14.0, so 10.4.  The
 // warps' fp32 sums meet in shared memory in the order of the warps (the result
 // does not depend on timing).
 #pragma once

@@ -7,8 +7,10 @@
 // group times a chunk of at most kTok of its tokens, so an instruction is as wide
 // as the tokens need (a multiple of 16 columns) and every copied byte of the
 // large operand is used.  On the pair kernel a group of 24 rows fills a tenth of
-// the 256 accumulator rows, its instructions take the time of 256, and the
-// stream of weights stops at 0.55 of the copy bandwidth.
+// the 256 accumulator rows and its instructions take the time of 256: 64 rows of
+// 262144 features take 212 us there and 127 here (weights at 0.89 of the copy
+// bandwidth; 16 rows 110, all of it), 2048 rows on 84 of 128 experts of 1408
+// features 62 us (0.84).
 //
 // Two CTAs per SM, each on its own, so that one's waits and stores are covered by
 // the other.  Each stage holds one block of 128 k: 16 KB of weights and the
