@@ -177,8 +177,9 @@ class Model:
         None goes back to bf16."""
         scratch, n = None, 0
         if experts is not None:
-            if experts.dtype != torch.uint8 or experts.numel() < lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg)):
-                raise ValueError("experts: a uint8 tensor from quantize_experts of the same configuration is needed")
+            if (experts.dtype != torch.uint8 or experts.device != self.weights.device or not experts.is_contiguous()
+                    or experts.numel() < lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg))):
+                raise ValueError("experts: a uint8 tensor from quantize_experts of the same configuration and device is needed")
             n = lib.dg_fp8_experts_scratch_bytes(self.ctx)
             scratch = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
         check(lib.dg_fp8_experts_use(self.ctx, _ptr(experts), _ptr(scratch), n))

@@ -172,3 +172,15 @@ def test_refusals():
     with pytest.raises(ValueError):
         model.use_fp8_experts(buf.view(torch.int8))
     model.close()
+
+
+def test_experts_elsewhere_are_refused():
+    import discrete_diffusion_moe_b200 as dg
+    cfg = dg.model_config(**TINY)
+    model = dg.Model(cfg, 1, seed=0)
+    n = dg.lib.dg_fp8_experts_bytes(ctypes.byref(cfg))
+    with pytest.raises(ValueError):
+        model.use_fp8_experts(torch.zeros(n, dtype=torch.uint8))                         # host memory
+    with pytest.raises(ValueError):
+        model.use_fp8_experts(torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2])  # every second byte
+    model.close()
