@@ -375,7 +375,7 @@ def test_offsets_beyond_32_bits():
     codes = torch.randint(0, 112, (G, N, K), device="cuda", dtype=torch.uint8)
     sb = torch.rand(G, ref.blocks(N), ref.blocks(K), device="cuda")
     assert codes.numel() > 2 ** 32
-    for sizes in ((1, 2), (40, 30), (300, 700)):     # every kernel
+    for sizes in ((1, 2), (40, 30), (300, 700), (500, 40600)):
         M = sum(sizes)
         a, sa = ref.random_operand(rng, M, K)
         off = torch.full((G + 1,), M, dtype=torch.int32, device="cuda")
@@ -383,8 +383,9 @@ def test_offsets_beyond_32_bits():
         out = dg.fp8_grouped_gemm(a, sa, codes.view(torch.float8_e4m3fn), sb, off)
         av, row = ref.dequantize_rows(a, sa), 0
         for g, n in zip((G - 2, G - 1), sizes):
-            want = ref.product(av[row:row + n], ref.dequantize_blocks(codes[g].view(torch.float8_e4m3fn), sb[g]))
-            _check(out[row:row + n], *want, K)
+            some = np.unique(np.r_[row:row + min(n, 20), row + n - min(n, 20):row + n])   # its first and last rows
+            want = ref.product(av[some], ref.dequantize_blocks(codes[g].view(torch.float8_e4m3fn), sb[g]))
+            _check(out[torch.from_numpy(some).cuda()], *want, K)
             row += n
 
 
@@ -401,6 +402,26 @@ def _in_range(got, want, want_abs, K):
     assert np.all(np.isfinite(out[np.abs(want) + bound < edge]))
     keep = np.isfinite(out)
     return got[torch.from_numpy(keep).cuda()], want[keep], want_abs[keep]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes,N,K", [([255, 256, 257, 0, 1, 300, 31, 420], 2000, 333), ([1790], 2299, 128),
+                                       ([600, 2, 0, 900], 4100, 1000)])
+def test_grouped_gemm_many_columns(sizes, N, K, out_dtype):
+    """Enough tiles that the widest ones are taken; groups that end inside a tile and a quarter of one."""
+    dg = _dg()
+    rng = np.random.default_rng(N + K)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    M, G = int(off[-1]), len(sizes)
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K, G=G)
+    w = torch.from_numpy(rng.standard_normal(M).astype(np.float32)).cuda()
+    got = dg.fp8_grouped_gemm(a, sa, b, sb, torch.from_numpy(off.astype(np.int32)).cuda(), row_weight=w, out_dtype=out_dtype)
+    av, wd = ref.dequantize_rows(a, sa), w.double().cpu().numpy()[:, None]
+    for g in range(G):
+        r = slice(off[g], off[g + 1])
+        want, want_abs = ref.product(av[r], ref.dequantize_blocks(b[g], sb[g]))
+        _check(got[r], want * wd[r], want_abs * np.abs(wd[r]), K, weighted=True)
 
 
 @pytest.mark.parametrize("N,K,out", [(40, 3054, torch.bfloat16), (24, 4096, torch.float32), (128, 2816, torch.bfloat16),
