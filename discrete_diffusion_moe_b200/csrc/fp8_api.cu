@@ -26,8 +26,7 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 template <class T, int ACT>
 dg_status launch_quant_rows(const QuantRowsParams& p, bool vec, cudaStream_t st) {
   const long long tasks = (long long)p.rows * p.KB;
-  const long long per_cta = (long long)kQuantThreads / 32 * 2 * kQuantTasks;
-  const dim3 grid((unsigned)ceil_div(tasks, per_cta));
+  const dim3 grid((unsigned)ceil_div(tasks, (long long)(kQuantThreads / kQuantLanes<T, ACT>)));
   if (vec) DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, true>, p));
   else     DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, false>, p));
   return DG_OK;

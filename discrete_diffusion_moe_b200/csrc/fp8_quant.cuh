@@ -13,11 +13,11 @@
 // holds a NaN or an infinity gets the scale NaN and codes 0: every product it
 // enters is NaN.
 //
-// One read of x, one write of the codes.  The weights (16 x 1408 x 2816 bf16: 34 us, 0.85
-// of the copy bandwidth) are bound by HBM, SwiGLU rows (32768 x 704 from
-// interleaved bf16 columns: 27 us where the bytes alone would take 18) by instruction
-// issue, busy in 82 % of the cycles with an exponential, a quotient, a maximum and a
-// conversion per element.
+// One read of x, one write of the codes.  Bound by HBM: the weights (16 x 1408 x 2816
+// bf16: 34 us, 0.86 of the copy bandwidth) and rows (32768 x 2816 bf16 47 us, 0.90).
+// SwiGLU rows (32768 x 704 from interleaved bf16 columns: 23.7 us where the bytes alone
+// would take 18) also by instruction issue, with an exponential, a reciprocal, a
+// maximum and a conversion per element.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -70,10 +70,18 @@ __device__ __forceinline__ float Raw8<float>::get(int i) const {
   return __uint_as_float(word_of(r[i >> 2], i & 3));
 }
 
-// silu(g) * u.  __expf and __fdividef: a few 2^-23 of relative error (the
-// exponent's rounding adds |g| 2^-24), far below the code's 2^-4 step; for
-// e^-g above 2^126 the quotient is 0, as silu's own limit.
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) * u with the approximate 2^x and reciprocal: a few 2^-23 of relative
+// error (the exponent's rounding adds |g| 2^-24), far below the code's 2^-4
+// step.  Subnormals are flushed, which spares the instructions that would keep
+// them: e^-g below 2^-126 counts as nothing beside 1, and above 2^126 its reciprocal is
+// 0, as silu's own limit.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  float e, q;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-kLog2e * g));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+  return g * q * u;
+}
 
 // ---- block scale and codes ------------------------------------------------------
 struct BlockScale {
@@ -110,108 +118,110 @@ struct QuantRowsParams {
   int rows, K, KB;
 };
 
-// Half a warp takes one (row, block of 128 columns): eight elements per lane, so
-// a row's block is one 256-byte load of bf16 and the maximum takes four
-// shuffles.  A warp takes 2 * kQuantTasks consecutive tasks and issues all
-// their loads first.  With SwiGLU the instructions count as much as the bytes
-// (23 M results of 92 MB: 37 instructions a result kept the schedulers at 80 %),
-// so a task's place takes one division per four tasks.  kVec: 16-byte loads and 8-byte
-// stores (every row of x 16-byte aligned and K a multiple of 8); otherwise lane
-// l takes elements l, l + 16, ... one by one.
-constexpr int kQuantTasks = 4;
-constexpr int kQuantThreads = 256;
+// A few lanes take one (row, block of 128 columns), groups of eight elements each:
+// group h of lane l starts at column (h * kLanes + l) * 8, so the lanes read
+// consecutive 16-byte words of bf16, all of a thread's at once.  Instructions count as
+// much as the bytes, so few lanes share what does not depend on the element (the task's
+// place, the shuffles of the maximum, the scale), as far as registers allow for enough
+// warps: 32768 x 2816 bf16 rows take 60 us with 16 lanes, 51 with 8, 47 with 4 and 71
+// with 2; SwiGLU of 32768 x 704 (twice the inputs a result) 23.7 with 8, 26 with 4;
+// fp32 rows, bound by HBM, 34.2 with 8 and 34.8 with 4.
+// kVec: 16-byte loads and 8-byte stores (every row of x 16-byte aligned and K a
+// multiple of 8); otherwise the elements are taken one by one, neighbours by
+// neighbouring lanes.
+constexpr int kQuantThreads = 128;
+template <class T, int ACT>
+constexpr int kQuantLanes = ACT == kActNone && sizeof(T) == 2 ? 4 : 8;
 
 template <class T, int ACT, bool kVec>
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantRowsParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, l = lane & 15;
-  // tasks below 2^31 (the host's check); one division, the later tasks by steps
-  const unsigned warp = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
-  const unsigned tasks = (unsigned)p.rows * (unsigned)p.KB;
-  const unsigned first = warp * (2 * kQuantTasks) + (lane >> 4);
-  int next_row = (int)(first / (unsigned)p.KB), next_kb = (int)(first - (unsigned)next_row * (unsigned)p.KB);
+  constexpr int kLanes = kQuantLanes<T, ACT>, kElems = kFp8Block / kLanes, kGroups = kElems / 8;
   constexpr int kIn = ACT == kActNone ? 1 : 2;
-  const T* const x = static_cast<const T*>(p.x);
+  const int l = threadIdx.x % kLanes;
+  // tasks below 2^31 (the host's check)
+  const unsigned task = blockIdx.x * (kQuantThreads / kLanes) + threadIdx.x / kLanes;
+  const int row = (int)(task / (unsigned)p.KB), k_lo = (int)(task - (unsigned)row * (unsigned)p.KB) * kFp8Block;
+  const bool work = task < (unsigned)p.rows * (unsigned)p.KB;
+  long long src = work ? row : -1;
+  if (p.index && work) {
+    src = __ldg(p.index + row);
+    if (src >= p.x_rows) src = -1;
+  }
+  const T* const xr = static_cast<const T*>(p.x) + (src < 0 ? 0 : src) * p.ldx;
 
-  int row[kQuantTasks], kb[kQuantTasks];
-  Raw8<T> raw[kVec ? kQuantTasks : 1][kIn];
-  float v[kQuantTasks][8];
+  float v[kElems];
+  if constexpr (kVec) {
+    Raw8<T> raw[kGroups][kIn];
 #pragma unroll
-  for (int u = 0; u < kQuantTasks; ++u) {
-    row[u] = first + 2 * u < tasks ? next_row : -1;
-    kb[u] = next_kb;
-    for (next_kb += 2; next_kb >= p.KB; next_kb -= p.KB) ++next_row;
-    long long src = row[u];
-    if (p.index && row[u] >= 0) {
-      src = __ldg(p.index + row[u]);
-      if (src >= p.x_rows) src = -1;
-    }
-    const T* xr = x + (src < 0 ? 0 : src) * p.ldx;
-    if constexpr (kVec) {
-      const int k0 = kb[u] * kFp8Block + l * 8;
-      const bool on = src >= 0 && k0 < p.K;  // K is a multiple of 8: all eight or none
+    for (int h = 0; h < kGroups; ++h) {
+      const int k = k_lo + (h * kLanes + l) * 8;
 #pragma unroll
-      for (int i = 0; i < kIn; ++i) raw[u][i].zero();
-      if (on) {
+      for (int i = 0; i < kIn; ++i) raw[h][i].zero();
+      if (src >= 0 && k < p.K) {  // K is a multiple of 8: all eight or none
         if constexpr (ACT == kActNone) {
-          raw[u][0].load(xr + k0);
+          raw[h][0].load(xr + k);
         } else if constexpr (ACT == kActSwiglu) {
-          raw[u][0].load(xr + k0);
-          raw[u][1].load(xr + p.K + k0);
+          raw[h][0].load(xr + k);
+          raw[h][1].load(xr + p.K + k);
         } else {
-          raw[u][0].load(xr + 2 * (long long)k0);
-          raw[u][1].load(xr + 2 * (long long)k0 + 8);
+          raw[h][0].load(xr + 2 * (long long)k);
+          raw[h][1].load(xr + 2 * (long long)k + 8);
         }
       }
-    } else {
+    }
+#pragma unroll
+    for (int h = 0; h < kGroups; ++h)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int k = kb[u] * kFp8Block + i * 16 + l;
-        const bool on = src >= 0 && k < p.K;
-        if constexpr (ACT == kActNone) {
-          v[u][i] = on ? elem_f32(xr + k) : 0.f;
-        } else {
-          const T* gp = ACT == kActSwiglu ? xr + k : xr + 2 * (long long)k;
-          const T* up = ACT == kActSwiglu ? xr + p.K + k : gp + 1;
-          v[u][i] = on ? swiglu(elem_f32(gp), elem_f32(up)) : 0.f;
-        }
+        float& o = v[8 * h + i];
+        if constexpr (ACT == kActNone) o = raw[h][0].get(i);
+        else if constexpr (ACT == kActSwiglu) o = swiglu(raw[h][0].get(i), raw[h][1].get(i));
+        else o = swiglu(raw[h][i >> 2].get((2 * i) & 7), raw[h][i >> 2].get(((2 * i) & 7) + 1));
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kElems; ++i) {
+      const int k = k_lo + i * kLanes + l;
+      const bool on = src >= 0 && k < p.K;
+      if constexpr (ACT == kActNone) {
+        v[i] = on ? elem_f32(xr + k) : 0.f;
+      } else {
+        const T* gp = ACT == kActSwiglu ? xr + k : xr + 2 * (long long)k;
+        const T* up = ACT == kActSwiglu ? xr + p.K + k : gp + 1;
+        v[i] = on ? swiglu(elem_f32(gp), elem_f32(up)) : 0.f;
       }
     }
   }
+  uint32_t m = 0u;
 #pragma unroll
-  for (int u = 0; u < kQuantTasks; ++u) {
-    if constexpr (kVec) {
+  for (int i = 0; i < kElems; ++i) m = max(m, abs_bits(v[i]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (ACT == kActNone) v[u][i] = raw[u][0].get(i);
-        else if constexpr (ACT == kActSwiglu) v[u][i] = swiglu(raw[u][0].get(i), raw[u][1].get(i));
-        else v[u][i] = swiglu(raw[u][i >> 2].get((2 * i) & 7), raw[u][i >> 2].get(((2 * i) & 7) + 1));
-      }
-    }
-    uint32_t m = 0u;
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!work) return;
+  const BlockScale s = block_scale(__uint_as_float(m));
+  uint8_t* const qr = p.q + (long long)row * p.ldq;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[u][i]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (row[u] < 0) continue;
-    const BlockScale s = block_scale(__uint_as_float(m));
-    uint8_t* const qr = p.q + (long long)row[u] * p.ldq + kb[u] * kFp8Block;
+  for (int h = 0; h < kGroups; ++h) {
+    const float* const e = v + 8 * h;
     uint32_t lo = 0u, hi = 0u;
     if (s.inv != 0.f) {  // codes 0 where the scale is NaN
-      lo = codes4(v[u][0] * s.inv, v[u][1] * s.inv, v[u][2] * s.inv, v[u][3] * s.inv);
-      hi = codes4(v[u][4] * s.inv, v[u][5] * s.inv, v[u][6] * s.inv, v[u][7] * s.inv);
+      lo = codes4(e[0] * s.inv, e[1] * s.inv, e[2] * s.inv, e[3] * s.inv);
+      hi = codes4(e[4] * s.inv, e[5] * s.inv, e[6] * s.inv, e[7] * s.inv);
     }
     if constexpr (kVec) {
-      if (kb[u] * kFp8Block + l * 8 < p.K) *reinterpret_cast<uint2*>(qr + l * 8) = make_uint2(lo, hi);
+      const int k = k_lo + (h * kLanes + l) * 8;
+      if (k < p.K) *reinterpret_cast<uint2*>(qr + k) = make_uint2(lo, hi);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (kb[u] * kFp8Block + i * 16 + l < p.K)
-          qr[i * 16 + l] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      for (int i = 0; i < 8; ++i) {
+        const int k = k_lo + (8 * h + i) * kLanes + l;
+        if (k < p.K) qr[k] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      }
     }
-    if (l == 0) p.scale[(long long)kb[u] * p.lds + row[u]] = s.scale;
   }
+  if (l == 0) p.scale[(long long)(k_lo / kFp8Block) * p.lds + row] = s.scale;
 }
 
 // ---- 128 x 128 blocks -------------------------------------------------------------------
