@@ -405,8 +405,9 @@ typedef enum dg_act {
    a row of zeros.  With a = max |x| of a block, raised to at least 2^-100:
    scale = a / 448, code = e4m3(x * (448 / a)) (fp32; to nearest even, at most
    +-448).  A block with a NaN or an infinity has scale NaN and codes 0.
-   SwiGLU is evaluated in fp32 with silu(z) = z / (1 + e^-z) and not rounded
-   before the quantisation. */
+   SwiGLU is evaluated in fp32 with silu(z) = z / (1 + e^-z), to 5 units of
+   2^-23 of its value (gates above -87), and not rounded before the
+   quantisation. */
 dg_status dg_fp8_quantize(const void* d_x, int32_t dtype, int64_t ldx, int64_t x_rows, const int32_t* d_index,
                           int32_t act, int64_t rows, int64_t cols, uint8_t* d_q, int64_t ldq, float* d_scale,
                           int64_t lds, void* stream);

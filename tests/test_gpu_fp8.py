@@ -118,6 +118,29 @@ def test_quantize_swiglu(rows, K, act, dtype):
 
 
 @pytest.mark.parametrize("act", ["swiglu", "swiglu_interleaved"])
+def test_quantize_swiglu_is_as_exact_as_fp32_allows(act):
+    """One element per block, so that its scale is the element's own magnitude
+    over 448: gates over silu's whole range, the far negative ones (e^-g above
+    2^126) too.  Relative error of fp32 steps: e^-|g| 2 units of 2^-23, the
+    product with it, the sum and the product with u half a unit each, the
+    quotient one, the scale's own quotient half a unit: 5 units.  Below g = -87.3
+    e^-|g| is subnormal, off by up to 2 of its steps of 2^-149."""
+    dg = _dg()
+    rng = np.random.default_rng(21)
+    g = np.concatenate([np.linspace(-88.6, -87.0, 33), rng.uniform(-90, 90, 4000), rng.uniform(-1, 1, 500)])
+    u = np.exp(rng.uniform(5, 20, g.size)) * np.where(g < -30, 2.0 ** 60, 1.0)
+    x = torch.from_numpy(np.stack((g, u), 1).astype(np.float32))
+    q, s = dg.fp8_quantize(x.cuda(), act=act)   # K = 1: both orders are (gate, up)
+    gd, ud = x.double().numpy().T
+    v = np.abs(ref.swiglu(gd, ud))
+    assert v.min() > ref.AMAX_MIN
+    rel = 5 * 2.0 ** -23 + np.where(gd < -87.3, 2 * 2.0 ** -149 * np.exp(np.abs(gd)), 0.0)
+    err = np.abs(s[0].double().cpu().numpy() * 448 / v - 1)
+    assert np.all(err <= rel), float((err / rel).max())
+    assert np.array_equal(q.double().cpu().numpy()[:, 0], 448 * np.sign(gd))
+
+
+@pytest.mark.parametrize("act", ["swiglu", "swiglu_interleaved"])
 def test_quantize_swiglu_special_values(act):
     """Gates of either infinity and far from zero, NaN gates and values: the
     blocks that hold no finite result are NaN, the others as the formula says."""
