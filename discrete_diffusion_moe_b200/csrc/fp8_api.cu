@@ -23,13 +23,16 @@ bool dtype_ok(int dt) { return dt == DG_BF16 || dt == DG_F16 || dt == DG_F32; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
+template <class T, int ACT, bool kVec>
+dg_status launch_quant_rows(const QuantRowsParams& p, cudaStream_t st) {
+  const long long tasks = (long long)p.rows * p.KB;
+  const dim3 grid((unsigned)ceil_div(tasks, (long long)(kQuantThreads / kQuantLanes<T, ACT, kVec>)));
+  DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, kVec>, p));
+  return DG_OK;
+}
 template <class T, int ACT>
 dg_status launch_quant_rows(const QuantRowsParams& p, bool vec, cudaStream_t st) {
-  const long long tasks = (long long)p.rows * p.KB;
-  const dim3 grid((unsigned)ceil_div(tasks, (long long)(kQuantThreads / kQuantLanes<T, ACT>)));
-  if (vec) DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, true>, p));
-  else     DG_CUDA(Launch(grid, dim3(kQuantThreads), 0, st)(quant_rows_kernel<T, ACT, false>, p));
-  return DG_OK;
+  return vec ? launch_quant_rows<T, ACT, true>(p, st) : launch_quant_rows<T, ACT, false>(p, st);
 }
 
 template <class T>

@@ -126,20 +126,22 @@ struct QuantRowsParams {
 // much as the bytes, so few lanes share what does not depend on the element (the task's
 // place, the shuffles of the maximum, the scale), as far as registers allow for enough
 // warps: 32768 x 2816 bf16 rows take 60 us with 16 lanes, 51 with 8, 47 with 4 and 71
-// with 2; SwiGLU of 32768 x 704 (twice the inputs a result) 23.7 with 8, 26 with 4;
-// fp32 rows, bound by HBM, 34.2 with 8 and 34.8 with 4.
+// with 2; SwiGLU of 32768 x 704 (twice the inputs a result; with a cheaper exponential)
+// 23.7 with 8, 26 with 4; fp32 rows, bound by HBM, 34.2 with 8 and 34.8 with 4.
 // kVec: 16-byte loads and 8-byte stores (every row of x 16-byte aligned and K a
 // multiple of 8); otherwise the elements are taken one by one, neighbours by
-// neighbouring lanes.
+// neighbouring lanes, and more of them share a block, so that a step touches whole
+// sectors: 32768 x 2815 bf16 rows take 208 us with 4 lanes, 110 with 8, 104 with 16;
+// fp32 113 with 8, 102 with 16.
 constexpr int kQuantThreads = 128;
-template <class T, int ACT>
-constexpr int kQuantLanes = ACT == kActNone && sizeof(T) == 2 ? 4 : 8;
+template <class T, int ACT, bool kVec>
+constexpr int kQuantLanes = !kVec ? 16 : (ACT == kActNone && sizeof(T) == 2 ? 4 : 8);
 
 template <class T, int ACT, bool kVec>
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(const QuantRowsParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int kLanes = kQuantLanes<T, ACT>, kElems = kFp8Block / kLanes, kGroups = kElems / 8;
+  constexpr int kLanes = kQuantLanes<T, ACT, kVec>, kElems = kFp8Block / kLanes, kGroups = kElems / 8;
   constexpr int kIn = ACT == kActNone ? 1 : 2;
   const int l = threadIdx.x % kLanes;
   // tasks below 2^31 (the host's check)
