@@ -127,6 +127,7 @@ def _load():
         "dg_test_attention": (I32, [P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, P, P, P]),
         "dg_test_workspace_buffer": (I32, [P, ctypes.c_char_p, ctypes.POINTER(P), ctypes.POINTER(S)]),
         "dg_test_wait_timeout": (I32, [P, ctypes.c_int64, P]),
+        "dg_test_fp8_hold": (I32, [I32, I32, I32, ctypes.c_int64]),
         "dg_test_struct_size": (S, [ctypes.c_char_p]),
         "dg_test_expected_embedding_topk": (I32, [P, ctypes.c_int64, I32, P, I32, I32, P, P]),
         "dg_router_probe": (I32, [P, I32, P, I32, P, P]),

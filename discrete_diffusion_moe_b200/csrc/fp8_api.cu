@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "../../include/dg.h"
+#include "../../include/dg_testing.h"
 #include "fp8_gemm.cuh"
 #include "fp8_quant.cuh"
 #include "fp8_small.cuh"
@@ -17,6 +18,10 @@ using namespace dg;
 namespace {
 
 constexpr long long kMaxDim = 2147483647ll - 4096;  // tile coordinates stay within 32 bits
+
+// The usual waits, or what dg_test_fp8_hold set for this thread's products.
+constexpr Fp8Waits kUsualWaits{kWaitLimitNs, kHoldNothing, 0, 0};
+thread_local Fp8Waits g_waits = kUsualWaits;
 
 size_t dtype_bytes(int dt) { return dt == DG_F32 ? 4 : 2; }
 bool dtype_ok(int dt) { return dt == DG_BF16 || dt == DG_F16 || dt == DG_F32; }
@@ -108,7 +113,8 @@ dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
   DG_TRY(set_smem_attr(fn, S::kSmem, true));
   const long long tiles = p.off ? std::min(p.G, p.M) + (long long)p.M / 256 : ceil_div(p.M, 256);  // at most
   const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, tiles * ceil_div(p.N, kW));
-  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kW, TO>, maps, p));
+  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kW, TO>, maps, p,
+                                                                                      g_waits));
   return DG_OK;
 }
 
@@ -127,7 +133,7 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
   const int splits = (int)std::max<long long>(1, std::min<long long>({slots / units, 8, p.KB / 2}));
   Launch l(dim3((unsigned)(splits > 1 ? splits * units : std::min(units, slots))), dim3(kStreamThreads), smem, st);
   if (splits > 1) l.cluster((unsigned)splits, 1, 1);
-  DG_CUDA(l(fp8_stream_kernel<kTok, TO>, maps, p, splits));
+  DG_CUDA(l(fp8_stream_kernel<kTok, TO>, maps, p, splits, g_waits));
   return DG_OK;
 }
 
@@ -293,4 +299,13 @@ extern "C" dg_status dg_fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const 
                        d_row_weight, d_out, out_dtype, ldo, &p));
   if (M == 0) return DG_OK;
   return product("dg_fp8_grouped_gemm", p, out_dtype, (cudaStream_t)stream);
+}
+
+extern "C" dg_status dg_test_fp8_hold(int32_t what, int32_t unit, int32_t block, int64_t limit_ns) {
+  if (what < kHoldNothing || what > kHoldScales || unit < 0 || block < 0 || limit_ns < 0 || limit_ns > 5000000000ll)
+    return fail(DG_ERR_INVALID_ARG, "dg_test_fp8_hold: bad arguments (a limit is at most 5 s)");
+  g_waits = kUsualWaits;
+  if (what != kHoldNothing)
+    g_waits = Fp8Waits{limit_ns ? (unsigned long long)limit_ns : kWaitLimitNs, what, unit, block};
+  return DG_OK;
 }

@@ -39,8 +39,11 @@
 //                 stage is free
 //   acc_empty[b]  rank 0's: the epilogue warps of both CTAs have read the buffer
 //   sc_full, sc_empty[i]  each CTA's own: a slot of scales is written, is read
-// All waits are bounded; after one runs out the CTA stops working and stores
-// NaN for what it could not compute.
+// All waits are bounded.  A role whose wait runs out stops: it copies, multiplies,
+// commits and releases nothing more, so that no barrier gets an arrival that its phase
+// does not expect and no other role takes old bytes for new ones; those that depend on it
+// run out in turn, in the other CTA too.  A CTA in which a wait ran out stores NaN from
+// then on, so whatever is stored as a number is the product.
 #pragma once
 
 #include "fp8_small.cuh"
@@ -60,6 +63,14 @@ constexpr int kFp8EpiWarps = 8;
 constexpr int kFp8Threads = 128 + 32 * kFp8EpiWarps;
 constexpr int kFp8RegsCopy = 72, kFp8RegsEpi = 216;
 static_assert(128 * kFp8RegsCopy + 32 * kFp8EpiWarps * kFp8RegsEpi <= kFp8Threads * 168, "register split");
+
+// The waits of a product: how long each may take, and for failure tests what a unit
+// leaves out of block `block`.
+enum { kHoldNothing = 0, kHoldCopies = 1, kHoldScales = 2 };
+struct Fp8Waits {
+  unsigned long long limit_ns;
+  int hold, unit, block;
+};
 
 // One lane of a converged warp.  The copies and MMAs take their descriptors from
 // uniform registers; issued from a branch on the lane number the compiler moves
@@ -99,27 +110,41 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
                : "memory");
   return v;
 }
-// Bounded wait of a whole warp without a result: when it runs out, the flag at
-// shared address `dead` is set (then later waits end at once) and the caller goes
-// on; the kernel's results are marked at their store.
-__device__ __forceinline__ void wait_or_die(uint32_t bar, uint32_t parity, uint32_t dead) {
-  if (!mbar_try_wait(bar, parity)) {
-    const unsigned long long t0 = globaltimer_ns();
-    uint32_t n = 0;
+// Whether no wait of this CTA has run out so far; the same answer for the whole warp.
+__device__ __forceinline__ bool alive(uint32_t dead) { return __all_sync(0xffffffffu, !ld_shared_flag(dead)); }
+// Bounded wait of one thread; false when it ran out, or another one of the CTA did
+// meanwhile (the flag at shared address `dead`).
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  uint32_t n = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-      if ((++n & 255u) == 0u && (ld_shared_flag(dead) || globaltimer_ns() - t0 > kWaitLimitNs)) {
-        asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
-        break;
-      }
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++n & 255u) == 0u && (ld_shared_flag(dead) || globaltimer_ns() - t0 > limit_ns)) {
+      asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
+      return false;
     }
   }
+  return true;
+}
+// The same of a whole warp: after false the warp's role has to stop.
+__device__ __forceinline__ bool wait_or_die(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns) {
+  return __all_sync(0xffffffffu, thread_wait(bar, parity, dead, limit_ns));
+}
+// The epilogue's: it goes on, but the lane that releases buffers (`releases`) does so no
+// more once its own wait ran out, and the results are marked at their store.  After a
+// wait of its own that ended well the phase is complete, even if another lane has
+// just given up on it.  (Leaving the loop over blocks on the warp's vote cost 5 % of
+// the time of 256-column units, with more spills.)
+__device__ __forceinline__ void wait_or_keep(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns,
+                                             bool& releases) {
+  if (!thread_wait(bar, parity, dead, limit_ns)) releases = false;
   __syncwarp();
 }
 // The same for what has to end before the CTA may leave (copies into its memory,
 // MMAs that read it): a failed wait elsewhere does not cut it short.
-__device__ __forceinline__ void wait_to_leave(uint32_t bar, uint32_t parity) {
-  mbar_wait(bar, parity, nullptr);
+__device__ __forceinline__ void wait_to_leave(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns) {
+  if (!mbar_wait(bar, parity, nullptr, limit_ns)) asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
   __syncwarp();
 }
 // 32 lanes x 32 consecutive fp32 columns of tensor memory; the registers are
@@ -345,7 +370,7 @@ __device__ __forceinline__ void store_turned(uint8_t* turn, const CUtensorMap* m
 
 template <int kW, class TO>
 __global__ void __launch_bounds__(kFp8Threads, 1)
-    fp8_pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8GemmParams p) {
+    fp8_pair_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8GemmParams p, const Fp8Waits wt) {
   using S = Fp8Shape<kW>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_tabs[3 * kFp8MaxGroups + 1];
@@ -416,8 +441,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
       auto a_box = [&](int rows) { return rows <= 0 ? -1 : (rows <= 16 ? 0 : (rows <= 64 ? 1 : 2)); };
       auto a_bytes = [&](int box) { return box < 0 ? 0u : (box == 0 ? 16u : (box == 1 ? 64u : 128u)) * 128u; };
-      for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
+      bool ok = true;
+      for (int u = pair; u < U && ok; u += pairs) {
         const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
+        const int held = wt.hold == kHoldCopies && u == wt.unit && rank == 1 ? wt.block : -1;
         const int mine = a_box(j.row1 - (j.row0 + (int)rank * 128));
         uint32_t tx = a_bytes(a_box(j.row1 - j.row0)) + a_bytes(a_box(j.row1 - j.row0 - 128));
         const int n = mma_cols(j);
@@ -427,8 +454,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const int yA = j.row0 + (int)rank * 128;
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-          wait_or_die(acc_full + s * 8u, phase, dead);
-          if (elect_one()) {
+          if (!(ok = wait_or_die(acc_full + s * 8u, phase, dead, wt.limit_ns))) break;
+          if (kb != held && elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s * 8u, tx);
             if (mine >= 0) tma_load_2d_pair(dstA + s * S::kStageA, &maps.a[mine], lead_bar + s * 8u, kb * 128, yA, pol_a);
             tma_load_2d_pair(dstB + s * S::kStageB, &maps.b[box], lead_bar + s * 8u, kb * 128, yB, pol_b);
@@ -444,7 +471,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // the leader's full barriers count both CTAs' bytes: wait until all have landed
       if (rank == 0) {
         const uint32_t first = issued > (uint32_t)S::kStages ? issued - S::kStages : 0;
-        for (uint32_t q = first; q < issued; ++q) wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1);
+        for (uint32_t q = first; q < issued; ++q)
+          wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead, wt.limit_ns);
       }
     } else if (warp == 1 || warp == 3) {
       if (rank == 0) {
@@ -456,15 +484,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         uint32_t s = m, phase = 0, b = m, b_phase = 1;
         int kb = (int)m;  // block of this warp within the unit
         const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
-        for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
+        bool ok = true;  // of this lane's waits: the issuing lane stops at its own
+        for (int u = pair; u < U && alive(dead); u += pairs) {
           const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
           const uint32_t idesc = idesc_e4m3_f32(256, mma_cols(j));
 #pragma unroll 1
           for (; kb < p.KB; kb += 2) {
-            wait_or_die(full + s * 8u, phase, dead);
-            wait_or_die(acc_empty + b * 8u, b_phase, dead);
+            ok = ok && thread_wait(full + s * 8u, phase, dead, wt.limit_ns);
+            ok = ok && thread_wait(acc_empty + b * 8u, b_phase, dead, wt.limit_ns);
+            __syncwarp();
             tc_fence_after();
-            if (elect_one()) {
+            if (elect_one() && ok) {
               const uint64_t da = descA + s * (S::kStageA / 16), db = descB + s * (S::kStageB / 16);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)  // 32 bytes on: 2 in the descriptor's 16-byte units
@@ -483,11 +513,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           kb -= p.KB;
         }
         if (elect_one()) umma_commit_pair(drain);
-        wait_to_leave(drain, 0);
+        wait_to_leave(drain, 0, dead, wt.limit_ns);
         // and the other CTA's last arrivals have come: none is on its way to a CTA that left
 #pragma unroll
         for (int i = 0; i < S::kBufs / 2; ++i) {
-          wait_or_die(acc_empty + b * 8u, b_phase, dead);
+          if (alive(dead)) wait_or_die(acc_empty + b * 8u, b_phase, dead, wt.limit_ns);
           b = (b + 2) % S::kBufs;
           if (b == m) b_phase ^= 1;
         }
@@ -498,8 +528,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       // load queues behind the copies of every stage, and waiting for one slot before
       // asking for the next set the pace of the whole kernel.
       uint32_t slot = 0, phase = 1;
-      for (int u = pair; u < U && !ld_shared_flag(dead); u += pairs) {
+      bool ok = true;
+      for (int u = pair; u < U && ok; u += pairs) {
         const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
+        const int held = wt.hold == kHoldScales && u == wt.unit && rank == 0 ? wt.block & ~3 : -1;
         const float* src[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) src[i] = p.sa + min(j.row0 + (int)rank * 128 + 32 * i + lane, j.row1 - 1);
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const float* const sb = p.sb + ((long long)j.group * p.NB + blk) * p.KB;
 #pragma unroll 1
         for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
-          wait_or_die(sc_empty + slot * 8u, phase, dead);
+          if (!(ok = wait_or_die(sc_empty + slot * 8u, phase, dead, wt.limit_ns))) break;
           const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -516,7 +548,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             for (int i = 0; i < 4; ++i) cp_async4(dst + (uint32_t)((32 * i + lane) * 4 + q) * 4u, src[i] + at);
           }
           if (lane < 8) cp_async4(dst + (uint32_t)(4 * 128 + lane) * 4u, sb + min(kb0 + (lane & 3), p.KB - 1));
-          cp_async_arrive(sc_full + slot * 8u);
+          if (kb0 != held) cp_async_arrive(sc_full + slot * 8u);
           if (++slot == S::kScaleSlots) {
             slot = 0;
             phase ^= 1;
@@ -535,6 +567,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const float4* const my_sa = reinterpret_cast<const float4*>(s_scale) + quarter * 32 + lane;
     const float4* const my_sb = reinterpret_cast<const float4*>(s_scale) + 128 + half;
     uint32_t s = 0, s_phase = 0, b = 0, slot = 0, slot_phase = 0, turn_next = 0;
+    bool releases = lane == 0;
     for (int u = pair; u < U; u += pairs) {
       const Fp8Job j = fp8_job<256>(p, tabs, u, m_tiles, n_tiles, kW);
       const int row_w0 = j.row0 + (int)rank * 128 + quarter * 32;
@@ -545,23 +578,22 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
       float4 sc4;  // the scales of four blocks
       auto read_scales = [&]() {
-        wait_or_die(sc_full + slot * 8u, slot_phase, dead);
+        wait_or_keep(sc_full + slot * 8u, slot_phase, dead, wt.limit_ns, releases);
         const float4 a4 = my_sa[slot * (S::kScaleSlot / 4)], b4 = my_sb[slot * (S::kScaleSlot / 4)];
         sc4 = make_float4(a4.x * b4.x, a4.y * b4.y, a4.z * b4.z, a4.w * b4.w);
         __syncwarp();
-        if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+        if (releases) mbar_arrive(sc_empty + slot * 8u);
         if (++slot == S::kScaleSlots) {
           slot = 0;
           slot_phase ^= 1;
         }
       };
-      read_scales();
       auto blocks = [&](auto works) {
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
           const int q = kb & 3;
           const float sc = q < 2 ? (q == 0 ? sc4.x : sc4.y) : (q == 2 ? sc4.z : sc4.w);
-          wait_or_die(acc_full + s * 8u, s_phase, dead);
+          wait_or_keep(acc_full + s * 8u, s_phase, dead, wt.limit_ns, releases);
           tc_fence_after();
           // Two loads at a time, and the buffer is released before the last sums are
           // added: what lies between the barrier and the release is on the path
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
               for (int c = 0; c < kTwo; ++c) tmem_wait32(r[c]);
               if (c0 + kTwo == kLd) {
                 tc_fence_before();
-                if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
+                if (releases) mbar_arrive_peer(release_to + b * 8u);
               }
 #pragma unroll
               for (int c = 0; c < kTwo; ++c)
@@ -588,7 +620,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             }
           } else {
             tc_fence_before();
-            if (lane == 0) mbar_arrive_peer(release_to + b * 8u);
+            if (releases) mbar_arrive_peer(release_to + b * 8u);
           }
           b = (b + 1) % S::kBufs;
           if (++s == S::kStages) {
@@ -599,11 +631,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         }
       };
       // two loops: a condition inside the loop cost a register move per loaded value
-      if (work) blocks(std::true_type{});
-      else      blocks(std::false_type{});
+      if (alive(dead)) {
+        read_scales();
+        if (work) blocks(std::true_type{});
+        else      blocks(std::false_type{});
+      }
       const int row = row_w0 + lane;
       // a wait that ran out: what was added is not the product
-      const float w = ld_shared_flag(dead) ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
+      const float w = !alive(dead) ? __uint_as_float(0x7fffffffu) : (p.row_w && row < j.row1 ? __ldg(p.row_w + row) : 1.0f);
       // the copy engine clips at the matrix's edges only, not at a group's last row
       const int rows = min(32, j.row1 - row_w0);
       const bool whole = S::kCols * sizeof(TO) >= 128 && p.vec_out && (rows == 32 || !p.off);

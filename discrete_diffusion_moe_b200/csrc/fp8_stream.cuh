@@ -68,7 +68,7 @@ __device__ __forceinline__ float ld_dsmem_f1(uint32_t addr) {
 template <int kTok, class TO>
 __global__ void __launch_bounds__(kStreamThreads, 2)
     fp8_stream_kernel(const __grid_constant__ Fp8StreamMaps maps, const __grid_constant__ Fp8GemmParams p,
-                      const int splits) {
+                      const int splits, const Fp8Waits wt) {
   using S = Fp8StreamShape<kTok>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ int s_dead;
@@ -136,16 +136,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     uint32_t it = 0;
     const uint64_t pol_w = l2_policy_evict_first(), pol_t = l2_policy_evict_last();
     const uint32_t dstA = smem_u32(sA), dstB = smem_u32(sB);
-    for (int u = first; u < U && !ld_shared_flag(dead); u += stride) {
+    bool ok = true;
+    for (int u = first; u < U && ok; u += stride) {
       const Fp8Job j = job(u);
+      const int held = wt.hold == kHoldCopies && u == wt.unit ? wt.block : -1;
       const int rows = j.row1 - j.row0;
       const int box = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
       const uint32_t tx = (uint32_t)(128 + (box == 0 ? 16 : (box == 1 ? 32 : kTok))) * 128u;
 #pragma unroll 1
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t s = it % S::kStages, bar = full + s * 8u;
-        wait_or_die(empty + s * 8u, ((it / S::kStages) & 1) ^ 1, dead);
-        if (elect_one()) {
+        if (!(ok = wait_or_die(empty + s * 8u, ((it / S::kStages) & 1) ^ 1, dead, wt.limit_ns))) break;
+        if (kb != held && elect_one()) {
           mbar_arrive_expect_tx(bar, tx);
           tma_load_2d_hint(dstA + s * S::kStageA, &maps.w, bar, kb * 128, j.group * p.N + j.n0, pol_w);
           tma_load_2d_hint(dstB + s * S::kStageB, &maps.t[box], bar, kb * 128, j.row0, pol_t);
@@ -153,19 +155,22 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         __syncwarp();
       }
     }
-    for (uint32_t q = it > (uint32_t)S::kStages ? it - S::kStages : 0; q < it; ++q) wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1);
+    for (uint32_t q = it > (uint32_t)S::kStages ? it - S::kStages : 0; q < it; ++q)
+      wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead, wt.limit_ns);
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     uint32_t it = 0;
     const uint64_t descA = sdesc_k128(smem_u32(sA)), descB = sdesc_k128(smem_u32(sB));
-    for (int u = first; u < U && !ld_shared_flag(dead); u += stride) {
+    bool ok = true;
+    for (int u = first; u < U && ok; u += stride) {
       const Fp8Job j = job(u);
       const uint32_t idesc = idesc_e4m3_f32(128, (j.row1 - j.row0 + 15) & ~15);
 #pragma unroll 1
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t s = it % S::kStages, b = it % S::kBufs;
-        wait_or_die(acc_empty + b * 8u, ((it / S::kBufs) & 1) ^ 1, dead);
-        wait_or_die(full + s * 8u, (it / S::kStages) & 1, dead);
+        if (!(ok = wait_or_die(acc_empty + b * 8u, ((it / S::kBufs) & 1) ^ 1, dead, wt.limit_ns) &&
+                   wait_or_die(full + s * 8u, (it / S::kStages) & 1, dead, wt.limit_ns)))
+          break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t da = descA + s * (S::kStageA / 16), db = descB + s * (S::kStageB / 16);
@@ -179,17 +184,19 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       }
     }
     if (elect_one()) umma_commit(drain);
-    wait_to_leave(drain, 0);
+    wait_to_leave(drain, 0, dead, wt.limit_ns);
   } else if (warp == 2) {
     // ---------------- scales: four blocks per slot ----------------
     uint32_t batch = 0;
-    for (int u = first; u < U && !ld_shared_flag(dead); u += stride) {
+    bool ok = true;
+    for (int u = first; u < U && ok; u += stride) {
       const Fp8Job j = job(u);
+      const int held = wt.hold == kHoldScales && u == wt.unit ? wt.block : -1;
       const float* const sb = p.sb + ((long long)j.group * p.NB + j.n0 / kFp8Block) * p.KB;
 #pragma unroll 1
       for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += 4, ++batch) {
         const uint32_t slot = batch % S::kScaleSlots;
-        wait_or_die(sc_empty + slot * 8u, ((batch / S::kScaleSlots) & 1) ^ 1, dead);
+        if (!(ok = wait_or_die(sc_empty + slot * 8u, ((batch / S::kScaleSlots) & 1) ^ 1, dead, wt.limit_ns))) break;
         const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -199,7 +206,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             cp_async4(dst + (uint32_t)(q * kTok + 32 * i + lane) * 4u, src + min(j.row0 + 32 * i + lane, j.row1 - 1));
         }
         if (lane < 4) cp_async4(dst + (uint32_t)(4 * kTok + lane) * 4u, sb + min(kb0 + lane, p.KB - 1));
-        cp_async_arrive(sc_full + slot * 8u);
+        if (held < kb0 || held > kb0 + 3) cp_async_arrive(sc_full + slot * 8u);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -208,6 +215,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     const int quarter = warp & 3;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     uint32_t it = 0, batch = 0;
+    bool releases = lane == 0;
     for (int u = first; u < U; u += stride) {
       const Fp8Job j = job(u);
       const int n_ld = (j.row1 - j.row0 + 31) / 32;  // 32-token parts
@@ -217,13 +225,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll
       for (int i = 0; i < kTok / 32; ++i) rw[i] = p.row_w ? __ldg(p.row_w + min(j.row0 + 32 * i + lane, j.row1 - 1)) : 1.f;
 #pragma unroll 1
-      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+      for (int kb = alive(dead) ? kb_lo : kb_hi; kb < kb_hi; ++kb, ++it) {
         const uint32_t slot = batch % S::kScaleSlots, b = it % S::kBufs;
         const int q = (kb - kb_lo) & 3;
-        if (q == 0) wait_or_die(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead);
+        if (q == 0) wait_or_keep(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead, wt.limit_ns, releases);
         const uint32_t at = smem_u32(s_scale + slot * S::kScaleSlot);
         const float sb = __int_as_float(ld_shared_flag(at + (uint32_t)(4 * kTok + q) * 4u));
-        wait_or_die(acc_full + b * 8u, (it / S::kBufs) & 1, dead);
+        wait_or_keep(acc_full + b * 8u, (it / S::kBufs) & 1, dead, wt.limit_ns, releases);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kTok / 32; ++c) {
@@ -243,9 +251,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty + b * 8u);
+        if (releases) mbar_arrive(acc_empty + b * 8u);
         if (q == 3 || kb + 1 == kb_hi) {
-          if (lane == 0) mbar_arrive(sc_empty + slot * 8u);
+          if (releases) mbar_arrive(sc_empty + slot * 8u);
           ++batch;
         }
       }
@@ -254,10 +262,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         float* const sums = reinterpret_cast<float*>(smem);  // every copy into the stages has been used
 #pragma unroll
         for (int i = 0; i < kTok; ++i)
-          if (i < rows) sums[i * 128 + f] = ld_shared_flag(dead) ? __uint_as_float(0x7fffffffu) : acc[i];
+          if (i < rows) sums[i * 128 + f] = acc[i];
         continue;
       }
-      const bool bad = ld_shared_flag(dead) != 0;  // a wait ran out: what was added is not the product
+      const bool bad = !alive(dead);  // a wait ran out: what was added is not the product
       TO* o = static_cast<TO*>(p.out) + (long long)j.row0 * p.ldo + n;
 #pragma unroll
       for (int c = 0; c < kTok / 32; ++c) {
@@ -277,6 +285,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, S::kBufs * kTok);
   if (splits > 1) {
+    if (s_dead)  // a wait ran out: what was added is not the product
+      for (int i = threadIdx.x; i < kTok * 128; i += kStreamThreads) reinterpret_cast<float*>(smem)[i] = __uint_as_float(0x7fffffffu);
     cluster_sync_all();  // every CTA's sums are written
     if (first < U) {
       // token i is added up (in the order of the ranks) and stored by CTA i % splits

@@ -390,7 +390,9 @@ dg_status dg_attention_static_scratch(const uint16_t* d_q, const uint16_t* d_k, 
    All calls only enqueue work on `stream` (of the current device) and use no
    workspace, so they may be captured into CUDA graphs and calls on different
    streams do not disturb one another.  Zero rows are a valid call that does
-   nothing.  Outputs must not overlap inputs. */
+   nothing.  Outputs must not overlap inputs.  Every wait inside a kernel is
+   bounded (2 s); should one run out, the kernel returns and what it could not
+   compute is NaN. */
 typedef enum dg_dtype { DG_BF16 = 0, DG_F16 = 1, DG_F32 = 2 } dg_dtype;
 typedef enum dg_act {
   DG_ACT_NONE = 0,

@@ -95,6 +95,17 @@ dg_status dg_test_attention(const uint16_t* d_q, const uint16_t* d_k, const uint
    (and clears) it and the context stays usable.  Asynchronous on `stream`. */
 dg_status dg_test_wait_timeout(dg_ctx* ctx, int64_t limit_ns, void* stream);
 
+/* Failure-path hook of the 8-bit products: the calling thread's following
+   products (dg_fp8_gemm, dg_fp8_grouped_gemm, the expert blocks of a context
+   on 8-bit experts) leave something out in unit `unit` of their kernel, so
+   that waits run out, and bound each wait by limit_ns (at most 5e9; 0: the
+   usual limit).  what 1: the copies of block `block` (128 columns of K; of a CTA
+   pair the second CTA's), 2: the scales of that block and those copied with
+   it (the first CTA's), 0: nothing, everything as usual again.  The kernels
+   return and store NaN for what they could not compute.  Kernels without
+   waits (at most eight rows) compute as usual. */
+dg_status dg_test_fp8_hold(int32_t what, int32_t unit, int32_t block, int64_t limit_ns);
+
 /* The top-k form of the expected embedding on its own (dg_sampler_config.
    selfcond_topk): for each of T rows of bf16 logits d_logits [T, V] (V a
    multiple of 256), the K (1 <= K <= min(1024, V)) largest (ties to the lower

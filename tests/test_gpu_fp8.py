@@ -570,6 +570,69 @@ def test_given_stream():
     assert torch.equal(q.view(torch.uint8), dg.fp8_quantize(want)[0].view(torch.uint8))
 
 
+def _held(dg, what, unit, block, call):
+    """`call` with something left out of one unit of its kernel, so that waits run out."""
+    dg.check(dg.lib.dg_test_fp8_hold(what, unit, block, 20_000_000))
+    try:
+        out = call()
+    finally:
+        dg.check(dg.lib.dg_test_fp8_hold(0, 0, 0, 0))
+    torch.cuda.synchronize()
+    return out
+
+
+# rows and columns of a unit and the units a CTA (pair) takes in turn, as the host chooses them on 148 SMs
+@pytest.mark.parametrize("what", [1, 2], ids=["copies", "scales"])
+@pytest.mark.parametrize("M,N,K,rows,cols,step", [
+    (600, 400, 1408, 256, 128, 74),      # pairs, 128 columns
+    (4096, 2048, 1408, 256, 256, 74),    # pairs, 256 columns, two units each
+    (64, 37888, 1408, 64, 128, 296),     # streaming, one unit each
+    (64, 75776, 1000, 64, 128, 296),     # streaming, two units each
+    (40, 512, 1408, 64, 128, 0)],        # streaming, a unit's blocks split among a cluster
+    ids=["pair128", "pair256", "stream", "stream2", "split"])
+def test_a_wait_that_runs_out_leaves_no_wrong_number(what, M, N, K, rows, cols, step):
+    """A unit whose copies or scales never come: the kernel returns, the unit and those
+    its CTAs would have taken after it hold NaN wherever they do not hold the product,
+    and all others are right.  Afterwards everything is as usual."""
+    dg = _dg()
+    rng = np.random.default_rng(M + N)
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K)
+    good = dg.fp8_gemm(a, sa, b, sb, out_dtype=torch.float32)
+    m_tiles, unit = (M + rows - 1) // rows, 2
+    out = torch.full_like(good, -3.0)
+    _held(dg, what, unit, 6, lambda: dg.fp8_gemm(a, sa, b, sb, out=out))
+
+    def tile(u):
+        return (slice(u % m_tiles * rows, (u % m_tiles + 1) * rows), slice(u // m_tiles * cols, (u // m_tiles + 1) * cols))
+    affected = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    for u in range(unit, m_tiles * ((N + cols - 1) // cols), step or 10 ** 6):
+        affected[tile(u)] = True
+    assert torch.equal(out[~affected], good[~affected])
+    nan = torch.isnan(out)
+    assert torch.all(nan | (out == good))
+    held = nan[tile(unit)]
+    if rows == 256 and what == 2:
+        held = held[:128]   # the CTA whose scales do not come; the other one may have had all it needs
+    assert torch.all(held)
+    assert torch.equal(dg.fp8_gemm(a, sa, b, sb, out_dtype=torch.float32), good)
+
+
+def test_grouped_wait_that_runs_out_leaves_no_wrong_number():
+    """The same with groups: rows of no group stay as they were."""
+    dg = _dg()
+    rng = np.random.default_rng(4)
+    off = torch.tensor([3, 300, 300, 900, 1000], dtype=torch.int32, device="cuda")
+    a, sa = ref.random_operand(rng, 1010, 1000)
+    b, sb = ref.random_weights(rng, 384, 1000, G=4)
+    outs = [torch.full((1010, 384), -3.0, device="cuda") for _ in range(2)]
+    dg.fp8_grouped_gemm(a, sa, b, sb, off, out=outs[0])
+    _held(dg, 1, 1, 3, lambda: dg.fp8_grouped_gemm(a, sa, b, sb, off, out=outs[1]))
+    nan = torch.isnan(outs[1])
+    assert nan.any() and torch.all(nan | (outs[0] == outs[1]))
+    assert torch.all(outs[1][:3] == -3.0) and torch.all(outs[1][1000:] == -3.0)
+
+
 def test_python_refusals():
     """Wrong shapes, types and strides are refused before any launch."""
     dg = _dg()
