@@ -1092,14 +1092,14 @@ static dg_status forward_layers(dg_ctx* c, const dg_kv* kv, int B, int nq, int L
       {
         ProfScope ps_(c, DG_PROF_EXPERT_GATE_UP, st);
         DG_TRY(dg_fp8_quantize(c->at<uint16_t>(L.xperm), DG_BF16, d, P, nullptr, DG_ACT_NONE, P, d, x8, d, sx, P, st));
-        DG_TRY(dg_fp8_grouped_gemm(x8, d, sx, P, c->w8 + W8.gu, d, (const float*)(c->w8 + W8.s_gu), off, E, P, 2 * f, d,
-                                   nullptr, y8, DG_BF16, 2 * f, st));
+        DG_TRY(fp8_grouped_gemm(x8, d, sx, P, c->w8 + W8.gu, d, (const float*)(c->w8 + W8.s_gu), off, E, P, 2 * f, d,
+                                nullptr, y8, DG_BF16, 2 * f, err, st));
       }
       {
         ProfScope ps_(c, DG_PROF_EXPERT_DOWN, st);
         DG_TRY(dg_fp8_quantize(y8, DG_BF16, 2 * f, P, nullptr, DG_ACT_SWIGLU_INTERLEAVED, P, f, h8, f, sh, P, st));
-        DG_TRY(dg_fp8_grouped_gemm(h8, f, sh, P, c->w8 + W8.dn, f, (const float*)(c->w8 + W8.s_dn), off, E, P, d, f,
-                                   c->at<float>(L.wperm), c->at<float>(L.yperm), DG_F32, d, st));
+        DG_TRY(fp8_grouped_gemm(h8, f, sh, P, c->w8 + W8.dn, f, (const float*)(c->w8 + W8.s_dn), off, E, P, d, f,
+                                c->at<float>(L.wperm), c->at<float>(L.yperm), DG_F32, d, err, st));
       }
       c->n_launch += 4;
     } else if (pair && DG_MOE_FUSED) {

@@ -20,7 +20,7 @@ namespace {
 constexpr long long kMaxDim = 2147483647ll - 4096;  // tile coordinates stay within 32 bits
 
 // The usual waits, or what dg_test_fp8_hold set for this thread's products.
-constexpr Fp8Waits kUsualWaits{kWaitLimitNs, kHoldNothing, 0, 0};
+constexpr Fp8Waits kUsualWaits{kWaitLimitNs, nullptr, kHoldNothing, 0, 0};
 thread_local Fp8Waits g_waits = kUsualWaits;
 
 size_t dtype_bytes(int dt) { return dt == DG_F32 ? 4 : 2; }
@@ -101,7 +101,7 @@ dg_status make_tmap_out(CUtensorMap* m, void* base, long long N, long long M, lo
 }
 
 template <int kW, class TO>
-dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
+dg_status launch_pair(const Fp8GemmParams& p, const Fp8Waits& wt, int pairs, cudaStream_t st) {
   using S = Fp8Shape<kW>;
   Fp8Maps maps;
   const int a_rows[3] = {16, 64, 128};
@@ -113,13 +113,12 @@ dg_status launch_pair(const Fp8GemmParams& p, int pairs, cudaStream_t st) {
   DG_TRY(set_smem_attr(fn, S::kSmem, true));
   const long long tiles = p.off ? std::min(p.G, p.M) + (long long)p.M / 256 : ceil_div(p.M, 256);  // at most
   const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, tiles * ceil_div(p.N, kW));
-  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kW, TO>, maps, p,
-                                                                                      g_waits));
+  DG_CUDA(Launch(dim3(grid), dim3(kFp8Threads), S::kSmem, st).cluster(2, 1, 1)(fp8_pair_kernel<kW, TO>, maps, p, wt));
   return DG_OK;
 }
 
 template <int kTok, class TO>
-dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
+dg_status launch_stream(const Fp8GemmParams& p, const Fp8Waits& wt, int sms, cudaStream_t st) {
   using S = Fp8StreamShape<kTok>;
   Fp8StreamMaps maps;
   const int rows[3] = {16, 32, kTok};
@@ -133,7 +132,7 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
   const int splits = (int)std::max<long long>(1, std::min<long long>({slots / units, 8, p.KB / 2}));
   Launch l(dim3((unsigned)(splits > 1 ? splits * units : std::min(units, slots))), dim3(kStreamThreads), smem, st);
   if (splits > 1) l.cluster((unsigned)splits, 1, 1);
-  DG_CUDA(l(fp8_stream_kernel<kTok, TO>, maps, p, splits, g_waits));
+  DG_CUDA(l(fp8_stream_kernel<kTok, TO>, maps, p, splits, wt));
   return DG_OK;
 }
 
@@ -154,7 +153,7 @@ dg_status launch_stream(const Fp8GemmParams& p, int sms, cudaStream_t st) {
 constexpr int kStreamRows = 64, kStreamGroupRows = 80, kPairRows = 32;
 
 template <class TO>
-dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
+dg_status launch_product(const Fp8GemmParams& p, const Fp8Waits& wt, cudaStream_t st) {
   const int sms = device_sms(), pairs = sms / 2;
   const long long groups = p.off ? std::min(p.G, p.M) : 1;  // that may have rows
   if (p.M <= kSmallRows && groups * ceil_div(p.N, 16) <= 2ll * kSmallCtas * sms) return launch_small<TO>(p, st);
@@ -162,16 +161,18 @@ dg_status launch_product(const Fp8GemmParams& p, cudaStream_t st) {
   const long long units128 = tiles * ceil_div(p.N, 128), units256 = tiles * ceil_div(p.N, 256);
   const bool one_wave = units128 <= pairs && 2 * units128 > pairs;
   if (p.M <= (p.off ? kStreamGroupRows : kStreamRows) * groups && !(p.M > kPairRows * groups && one_wave))
-    return launch_stream<64, TO>(p, sms, st);
-  if (3 * ceil_div(units128, pairs) < 5 * ceil_div(units256, pairs)) return launch_pair<128, TO>(p, pairs, st);
-  return launch_pair<256, TO>(p, pairs, st);
+    return launch_stream<64, TO>(p, wt, sms, st);
+  if (3 * ceil_div(units128, pairs) < 5 * ceil_div(units256, pairs)) return launch_pair<128, TO>(p, wt, pairs, st);
+  return launch_pair<256, TO>(p, wt, pairs, st);
 }
 
-dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, cudaStream_t st) {
+dg_status product(const char* who, const Fp8GemmParams& p, int out_dtype, int* err, cudaStream_t st) {
+  Fp8Waits wt = g_waits;
+  wt.err = err;
   switch (out_dtype) {
-    case DG_BF16: return launch_product<__nv_bfloat16>(p, st);
-    case DG_F16: return launch_product<__half>(p, st);
-    case DG_F32: return launch_product<float>(p, st);
+    case DG_BF16: return launch_product<__nv_bfloat16>(p, wt, st);
+    case DG_F16: return launch_product<__half>(p, wt, st);
+    case DG_F32: return launch_product<float>(p, wt, st);
     default: return fail(DG_ERR_INVALID_ARG, "%s: output type %d", who, out_dtype);
   }
 }
@@ -286,19 +287,27 @@ extern "C" dg_status dg_fp8_gemm(const uint8_t* d_a, int64_t lda, const float* d
   DG_TRY(check_product("dg_fp8_gemm", d_a, lda, d_a_scale, lds, d_b, ldb, d_b_scale, nullptr, 1, M, N, K, d_row_weight,
                        d_out, out_dtype, ldo, &p));
   if (M == 0) return DG_OK;
-  return product("dg_fp8_gemm", p, out_dtype, (cudaStream_t)stream);
+  return product("dg_fp8_gemm", p, out_dtype, nullptr, (cudaStream_t)stream);
+}
+
+dg_status dg::fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds, const uint8_t* d_b,
+                               int64_t ldb, const float* d_b_scale, const int32_t* d_off, int64_t groups, int64_t M,
+                               int64_t N, int64_t K, const float* d_row_weight, void* d_out, int32_t out_dtype,
+                               int64_t ldo, int* err, cudaStream_t st) {
+  Fp8GemmParams p;
+  if (!d_off) return fail(DG_ERR_INVALID_ARG, "dg_fp8_grouped_gemm: null offsets");
+  DG_TRY(check_product("dg_fp8_grouped_gemm", d_a, lda, d_a_scale, lds, d_b, ldb, d_b_scale, d_off, groups, M, N, K,
+                       d_row_weight, d_out, out_dtype, ldo, &p));
+  if (M == 0) return DG_OK;
+  return product("dg_fp8_grouped_gemm", p, out_dtype, err, st);
 }
 
 extern "C" dg_status dg_fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds,
                                          const uint8_t* d_b, int64_t ldb, const float* d_b_scale, const int32_t* d_off,
                                          int64_t groups, int64_t M, int64_t N, int64_t K, const float* d_row_weight,
                                          void* d_out, int32_t out_dtype, int64_t ldo, void* stream) {
-  Fp8GemmParams p;
-  if (!d_off) return fail(DG_ERR_INVALID_ARG, "dg_fp8_grouped_gemm: null offsets");
-  DG_TRY(check_product("dg_fp8_grouped_gemm", d_a, lda, d_a_scale, lds, d_b, ldb, d_b_scale, d_off, groups, M, N, K,
-                       d_row_weight, d_out, out_dtype, ldo, &p));
-  if (M == 0) return DG_OK;
-  return product("dg_fp8_grouped_gemm", p, out_dtype, (cudaStream_t)stream);
+  return fp8_grouped_gemm(d_a, lda, d_a_scale, lds, d_b, ldb, d_b_scale, d_off, groups, M, N, K, d_row_weight, d_out,
+                          out_dtype, ldo, nullptr, (cudaStream_t)stream);
 }
 
 extern "C" dg_status dg_test_fp8_hold(int32_t what, int32_t unit, int32_t block, int64_t limit_ns) {
@@ -306,6 +315,6 @@ extern "C" dg_status dg_test_fp8_hold(int32_t what, int32_t unit, int32_t block,
     return fail(DG_ERR_INVALID_ARG, "dg_test_fp8_hold: bad arguments (a limit is at most 5 s)");
   g_waits = kUsualWaits;
   if (what != kHoldNothing)
-    g_waits = Fp8Waits{limit_ns ? (unsigned long long)limit_ns : kWaitLimitNs, what, unit, block};
+    g_waits = Fp8Waits{limit_ns ? (unsigned long long)limit_ns : kWaitLimitNs, nullptr, what, unit, block};
   return DG_OK;
 }

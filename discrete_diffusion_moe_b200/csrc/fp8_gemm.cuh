@@ -64,11 +64,13 @@ constexpr int kFp8Threads = 128 + 32 * kFp8EpiWarps;
 constexpr int kFp8RegsCopy = 72, kFp8RegsEpi = 216;
 static_assert(128 * kFp8RegsCopy + 32 * kFp8EpiWarps * kFp8RegsEpi <= kFp8Threads * 168, "register split");
 
-// The waits of a product: how long each may take, and for failure tests what a unit
+// The waits of a product: how long each may take, the error word of a context (or
+// null) that gets kDevErrTimeout when one runs out, and for failure tests what a unit
 // leaves out of block `block`.
 enum { kHoldNothing = 0, kHoldCopies = 1, kHoldScales = 2 };
 struct Fp8Waits {
   unsigned long long limit_ns;
+  int* err;
   int hold, unit, block;
 };
 
@@ -114,37 +116,40 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
 __device__ __forceinline__ bool alive(uint32_t dead) { return __all_sync(0xffffffffu, !ld_shared_flag(dead)); }
 // Bounded wait of one thread; false when it ran out, or another one of the CTA did
 // meanwhile (the flag at shared address `dead`).
-__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns) {
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, uint32_t dead, const Fp8Waits& wt) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
   uint32_t n = 0;
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
-    if ((++n & 255u) == 0u && (ld_shared_flag(dead) || globaltimer_ns() - t0 > limit_ns)) {
-      asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
-      return false;
+    if ((++n & 255u) == 0u) {
+      if (ld_shared_flag(dead)) return false;
+      if (globaltimer_ns() - t0 > wt.limit_ns) {
+        asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
+        set_error(wt.err, kDevErrTimeout);
+        return false;
+      }
     }
   }
   return true;
 }
 // The same of a whole warp: after false the warp's role has to stop.
-__device__ __forceinline__ bool wait_or_die(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns) {
-  return __all_sync(0xffffffffu, thread_wait(bar, parity, dead, limit_ns));
+__device__ __forceinline__ bool wait_or_die(uint32_t bar, uint32_t parity, uint32_t dead, const Fp8Waits& wt) {
+  return __all_sync(0xffffffffu, thread_wait(bar, parity, dead, wt));
 }
 // The epilogue's: it goes on, but the lane that releases buffers (`releases`) does so no
 // more once its own wait ran out, and the results are marked at their store.  After a
 // wait of its own that ended well the phase is complete, even if another lane has
 // just given up on it.  (Leaving the loop over blocks on the warp's vote cost 5 % of
 // the time of 256-column units, with more spills.)
-__device__ __forceinline__ void wait_or_keep(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns,
-                                             bool& releases) {
-  if (!thread_wait(bar, parity, dead, limit_ns)) releases = false;
+__device__ __forceinline__ void wait_or_keep(uint32_t bar, uint32_t parity, uint32_t dead, const Fp8Waits& wt, bool& releases) {
+  if (!thread_wait(bar, parity, dead, wt)) releases = false;
   __syncwarp();
 }
 // The same for what has to end before the CTA may leave (copies into its memory,
 // MMAs that read it): a failed wait elsewhere does not cut it short.
-__device__ __forceinline__ void wait_to_leave(uint32_t bar, uint32_t parity, uint32_t dead, unsigned long long limit_ns) {
-  if (!mbar_wait(bar, parity, nullptr, limit_ns)) asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
+__device__ __forceinline__ void wait_to_leave(uint32_t bar, uint32_t parity, uint32_t dead, const Fp8Waits& wt) {
+  if (!mbar_wait(bar, parity, wt.err, wt.limit_ns)) asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(dead) : "memory");
   __syncwarp();
 }
 // 32 lanes x 32 consecutive fp32 columns of tensor memory; the registers are
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const int yA = j.row0 + (int)rank * 128;
 #pragma unroll 1
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!(ok = wait_or_die(acc_full + s * 8u, phase, dead, wt.limit_ns))) break;
+          if (!(ok = wait_or_die(acc_full + s * 8u, phase, dead, wt))) break;
           if (kb != held && elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full + s * 8u, tx);
             if (mine >= 0) tma_load_2d_pair(dstA + s * S::kStageA, &maps.a[mine], lead_bar + s * 8u, kb * 128, yA, pol_a);
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       if (rank == 0) {
         const uint32_t first = issued > (uint32_t)S::kStages ? issued - S::kStages : 0;
         for (uint32_t q = first; q < issued; ++q)
-          wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead, wt.limit_ns);
+          wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead, wt);
       }
     } else if (warp == 1 || warp == 3) {
       if (rank == 0) {
@@ -490,8 +495,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           const uint32_t idesc = idesc_e4m3_f32(256, mma_cols(j));
 #pragma unroll 1
           for (; kb < p.KB; kb += 2) {
-            ok = ok && thread_wait(full + s * 8u, phase, dead, wt.limit_ns);
-            ok = ok && thread_wait(acc_empty + b * 8u, b_phase, dead, wt.limit_ns);
+            ok = ok && thread_wait(full + s * 8u, phase, dead, wt);
+            ok = ok && thread_wait(acc_empty + b * 8u, b_phase, dead, wt);
             __syncwarp();
             tc_fence_after();
             if (elect_one() && ok) {
@@ -513,11 +518,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
           kb -= p.KB;
         }
         if (elect_one()) umma_commit_pair(drain);
-        wait_to_leave(drain, 0, dead, wt.limit_ns);
+        wait_to_leave(drain, 0, dead, wt);
         // and the other CTA's last arrivals have come: none is on its way to a CTA that left
 #pragma unroll
         for (int i = 0; i < S::kBufs / 2; ++i) {
-          if (alive(dead)) wait_or_die(acc_empty + b * 8u, b_phase, dead, wt.limit_ns);
+          if (alive(dead)) wait_or_die(acc_empty + b * 8u, b_phase, dead, wt);
           b = (b + 2) % S::kBufs;
           if (b == m) b_phase ^= 1;
         }
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const float* const sb = p.sb + ((long long)j.group * p.NB + blk) * p.KB;
 #pragma unroll 1
         for (int kb0 = 0; kb0 < p.KB; kb0 += 4) {
-          if (!(ok = wait_or_die(sc_empty + slot * 8u, phase, dead, wt.limit_ns))) break;
+          if (!(ok = wait_or_die(sc_empty + slot * 8u, phase, dead, wt))) break;
           const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       for (int i = 0; i < S::kCols; ++i) acc[i] = 0.f;
       float4 sc4;  // the scales of four blocks
       auto read_scales = [&]() {
-        wait_or_keep(sc_full + slot * 8u, slot_phase, dead, wt.limit_ns, releases);
+        wait_or_keep(sc_full + slot * 8u, slot_phase, dead, wt, releases);
         const float4 a4 = my_sa[slot * (S::kScaleSlot / 4)], b4 = my_sb[slot * (S::kScaleSlot / 4)];
         sc4 = make_float4(a4.x * b4.x, a4.y * b4.y, a4.z * b4.z, a4.w * b4.w);
         __syncwarp();
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         for (int kb = 0; kb < p.KB; ++kb) {
           const int q = kb & 3;
           const float sc = q < 2 ? (q == 0 ? sc4.x : sc4.y) : (q == 2 ? sc4.z : sc4.w);
-          wait_or_keep(acc_full + s * 8u, s_phase, dead, wt.limit_ns, releases);
+          wait_or_keep(acc_full + s * 8u, s_phase, dead, wt, releases);
           tc_fence_after();
           // Two loads at a time, and the buffer is released before the last sums are
           // added: what lies between the barrier and the release is on the path

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll 1
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t s = it % S::kStages, bar = full + s * 8u;
-        if (!(ok = wait_or_die(empty + s * 8u, ((it / S::kStages) & 1) ^ 1, dead, wt.limit_ns))) break;
+        if (!(ok = wait_or_die(empty + s * 8u, ((it / S::kStages) & 1) ^ 1, dead, wt))) break;
         if (kb != held && elect_one()) {
           mbar_arrive_expect_tx(bar, tx);
           tma_load_2d_hint(dstA + s * S::kStageA, &maps.w, bar, kb * 128, j.group * p.N + j.n0, pol_w);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       }
     }
     for (uint32_t q = it > (uint32_t)S::kStages ? it - S::kStages : 0; q < it; ++q)
-      wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead, wt.limit_ns);
+      wait_to_leave(full + (q % S::kStages) * 8u, (q / S::kStages) & 1, dead, wt);
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
     uint32_t it = 0;
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll 1
       for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
         const uint32_t s = it % S::kStages, b = it % S::kBufs;
-        if (!(ok = wait_or_die(acc_empty + b * 8u, ((it / S::kBufs) & 1) ^ 1, dead, wt.limit_ns) &&
-                   wait_or_die(full + s * 8u, (it / S::kStages) & 1, dead, wt.limit_ns)))
+        if (!(ok = wait_or_die(acc_empty + b * 8u, ((it / S::kBufs) & 1) ^ 1, dead, wt) &&
+                   wait_or_die(full + s * 8u, (it / S::kStages) & 1, dead, wt)))
           break;
         tc_fence_after();
         if (elect_one()) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       }
     }
     if (elect_one()) umma_commit(drain);
-    wait_to_leave(drain, 0, dead, wt.limit_ns);
+    wait_to_leave(drain, 0, dead, wt);
   } else if (warp == 2) {
     // ---------------- scales: four blocks per slot ----------------
     uint32_t batch = 0;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll 1
       for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += 4, ++batch) {
         const uint32_t slot = batch % S::kScaleSlots;
-        if (!(ok = wait_or_die(sc_empty + slot * 8u, ((batch / S::kScaleSlots) & 1) ^ 1, dead, wt.limit_ns))) break;
+        if (!(ok = wait_or_die(sc_empty + slot * 8u, ((batch / S::kScaleSlots) & 1) ^ 1, dead, wt))) break;
         const uint32_t dst = smem_u32(s_scale + slot * S::kScaleSlot);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -228,10 +228,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       for (int kb = alive(dead) ? kb_lo : kb_hi; kb < kb_hi; ++kb, ++it) {
         const uint32_t slot = batch % S::kScaleSlots, b = it % S::kBufs;
         const int q = (kb - kb_lo) & 3;
-        if (q == 0) wait_or_keep(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead, wt.limit_ns, releases);
+        if (q == 0) wait_or_keep(sc_full + slot * 8u, (batch / S::kScaleSlots) & 1, dead, wt, releases);
         const uint32_t at = smem_u32(s_scale + slot * S::kScaleSlot);
         const float sb = __int_as_float(ld_shared_flag(at + (uint32_t)(4 * kTok + q) * 4u));
-        wait_or_keep(acc_full + b * 8u, (it / S::kBufs) & 1, dead, wt.limit_ns, releases);
+        wait_or_keep(acc_full + b * 8u, (it / S::kBufs) & 1, dead, wt, releases);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kTok / 32; ++c) {

@@ -73,6 +73,13 @@ struct Launch {
   }
 };
 
+// dg_fp8_grouped_gemm with a context's error word `err` (or null), which gets
+// kDevErrTimeout when a wait of the kernel runs out.
+dg_status fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t lds, const uint8_t* d_b,
+                           int64_t ldb, const float* d_b_scale, const int32_t* d_off, int64_t groups, int64_t M,
+                           int64_t N, int64_t K, const float* d_row_weight, void* d_out, int32_t out_dtype, int64_t ldo,
+                           int* err, cudaStream_t st);
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,

@@ -392,7 +392,8 @@ dg_status dg_attention_static_scratch(const uint16_t* d_q, const uint16_t* d_k, 
    streams do not disturb one another.  Zero rows are a valid call that does
    nothing.  Outputs must not overlap inputs.  Every wait inside a kernel is
    bounded (2 s); should one run out, the kernel returns and what it could not
-   compute is NaN. */
+   compute is NaN (in a context on 8-bit experts dg_check_device_error reports
+   it, too). */
 typedef enum dg_dtype { DG_BF16 = 0, DG_F16 = 1, DG_F32 = 2 } dg_dtype;
 typedef enum dg_act {
   DG_ACT_NONE = 0,

@@ -151,6 +151,42 @@ def test_blocks_and_autoregressive_steps_on_shared_experts():
     second.close()
 
 
+@pytest.mark.parametrize("n_experts,tokens", [(4, 256), (16, 40)], ids=["pairs", "streaming"])
+def test_an_expert_product_whose_wait_runs_out_is_reported(n_experts, tokens):
+    """Copies that never come in an expert product of an encode pass (of one layer,
+    after whose expert block nothing reads the result): the error word says so, and
+    after it the context gives what it gave before."""
+    import discrete_diffusion_moe_b200 as dg
+    cfg = dg.model_config(**dict(TINY, n_layers=1, n_experts=n_experts, top_k=2))
+    model = dg.Model(cfg, 1, seed=0)
+    model.use_fp8_experts(model.quantize_experts())
+    kv = dg.KVCache(cfg, 1, tokens + 256)
+    toks = torch.from_numpy(synth.context_tokens(1, tokens, 3, cfg.vocab).astype(np.int32)).cuda()
+    y = _buffer(dg, model, "yperm", torch.float32, (tokens * 2, cfg.d_model))
+    inv = _buffer(dg, model, "inv", torch.int32, (tokens * 2,))
+
+    def encode():
+        """The expert block's rows by token (their order within an expert may differ between passes)."""
+        kv.s.length = 0
+        model.encode(kv, toks)
+        return y[inv.long()]
+    want = encode()
+    model.check_device()
+    dg.check(dg.lib.dg_test_fp8_hold(1, 0, 0, 20_000_000))
+    try:
+        got = encode()
+    finally:
+        dg.check(dg.lib.dg_test_fp8_hold(0, 0, 0, 0))
+    with pytest.raises(dg.DgError) as e:
+        model.check_device()
+    assert e.value.status == dg.DG_ERR_TIMEOUT
+    nan = torch.isnan(got)
+    assert nan.any() and torch.all(nan | (got == want))
+    assert torch.equal(encode(), want)
+    model.check_device()
+    model.close()
+
+
 def test_refusals():
     import discrete_diffusion_moe_b200 as dg
     cfg = dg.model_config(**TINY)
