@@ -268,10 +268,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_relinquish();
   }
   grid_dep_wait();
-  grid_dep_launch();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before the tensor memory is held
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t t_s = tmem_base, t_o = tmem_base + 64, t_p = tmem_base + S::P_COL;
 

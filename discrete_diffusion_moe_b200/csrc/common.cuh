@@ -28,7 +28,11 @@ __device__ __forceinline__ void set_error(int* err, int code) {
 // grid_dep_wait() before it reads or writes memory that another kernel
 // writes or reads (before it, only its own shared / tensor memory set-up and
 // the tensor maps), and grid_dep_launch() right after, which lets the next
-// kernel's CTAs be scheduled once every CTA of this grid has got that far.
+// kernel's CTAs be scheduled once every CTA of this grid has got that far (the first
+// thread of a CTA that calls it counts).  A kernel with tensor memory calls it behind
+// the barrier that follows its allocation: a dependent's CTA may allocate before its
+// own grid_dep_wait, and if it took columns for which a CTA of this grid still
+// waited, both grids would wait for good.
 // Outside such a launch both are no-ops.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

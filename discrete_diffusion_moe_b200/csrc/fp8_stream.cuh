@@ -118,11 +118,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     tmem_relinquish();
   }
   grid_dep_wait();
-  grid_dep_launch();
   if (p.off && warp == 4) fp8_tables<kTok>(p, tabs, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before the tensor memory is held
   const uint32_t tmem_base = *tmem_slot;
   const int f_tiles = (p.N + 127) / 128;
   const int chunks = p.off ? tabs.first[p.G] : (p.M + kTok - 1) / kTok;

@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 2)
     for (int i = 0; i < 3; ++i) tma_prefetch_desc(&tmB.m[i]);
   }
   grid_dep_wait();
-  grid_dep_launch();
   if (warp >= 2 && p.group_off) {
     for (int g = threadIdx.x - 64; g <= p.n_groups; g += gemm_threads<Epi>() - 64) {
       tabs.chunk_off[g] = __ldg(p.chunk_off + g);
@@ -239,6 +238,7 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before the tensor memory is held
   const uint32_t tmem_base = *tmem_slot;
 
   const int U = dense ? U_dense : pair_num_units(p, tabs);

@@ -123,7 +123,6 @@ __global__ void __launch_bounds__(gemm_threads<EpiU>(), 2)
     }
   }
   grid_dep_wait();
-  grid_dep_launch();
   if (warp >= 2) {
     for (int g = threadIdx.x - 64; g <= mp.up.n_groups; g += gemm_threads<EpiU>() - 64) {
       tabs.chunk_off[g] = __ldg(mp.up.chunk_off + g);
@@ -139,6 +138,7 @@ __global__ void __launch_bounds__(gemm_threads<EpiU>(), 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // not before the tensor memory is held
   const uint32_t tmem_base = *tmem_slot;
 
   const int chunks = tabs.chunk_off[mp.up.n_groups];
