@@ -168,7 +168,8 @@ class Model:
         """The model's expert matrices in 8 bits (dg_fp8_experts_quantize), for
         use_fp8_experts of this model or of one that shares its weights."""
         n = lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg))
-        experts = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
+        with torch.cuda.stream(stream):   # memory of the stream that writes it
+            experts = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
         check(lib.dg_fp8_experts_quantize(self.ctx, _ptr(experts), n, _stream(stream)))
         return experts
 

@@ -187,6 +187,31 @@ def test_an_expert_product_whose_wait_runs_out_is_reported(n_experts, tokens):
     model.close()
 
 
+def _busy(stream, ms=60):
+    """Keeps `stream` busy for about `ms` milliseconds."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 2e6))
+
+
+def test_experts_quantised_on_another_stream_are_its_memory():
+    """The buffer is not one that work on the current stream still writes to."""
+    import discrete_diffusion_moe_b200 as dg
+    cfg = dg.model_config(**TINY)
+    model = dg.Model(cfg, 1, seed=0)
+    want = model.quantize_experts()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(2):   # the second time the allocator has blocks of this size to give
+        _busy(torch.cuda.current_stream())
+        old = torch.empty(want.numel(), dtype=torch.uint8, device="cuda")
+        old.fill_(7)
+        del old          # free for the current stream, whose fill is still to come
+        got = model.quantize_experts(stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    model.close()
+
+
 def test_refusals():
     import discrete_diffusion_moe_b200 as dg
     cfg = dg.model_config(**TINY)
