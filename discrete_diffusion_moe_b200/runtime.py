@@ -152,6 +152,7 @@ class Model:
         check(lib.dg_context_create_ex(ctypes.byref(cfg), _ptr(self.weights), _ptr(self.workspace), nws, batch,
                                        prefill_tokens, ctypes.byref(ctx)))
         self.ctx = ctx
+        self.experts8 = self.scratch8 = None
 
     def close(self):
         if getattr(self, "ctx", None):
@@ -175,16 +176,21 @@ class Model:
 
     def use_fp8_experts(self, experts: torch.Tensor = None):
         """Run the expert blocks on 8-bit matrices (dg_fp8_experts_use);
-        None goes back to bf16."""
-        scratch, n = None, 0
-        if experts is not None:
-            if (experts.dtype != torch.uint8 or experts.device != self.weights.device or not experts.is_contiguous()
-                    or experts.numel() < lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg))):
-                raise ValueError("experts: a uint8 tensor from quantize_experts of the same configuration and device is needed")
-            n = lib.dg_fp8_experts_scratch_bytes(self.ctx)
-            scratch = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
-        check(lib.dg_fp8_experts_use(self.ctx, _ptr(experts), _ptr(scratch), n))
-        self.experts8, self.scratch8 = experts, scratch   # keeps them alive
+        None goes back to bf16.  Waits for the device's work where the matrices
+        change: passes enqueued before, on whatever stream, may still read the
+        old ones."""
+        if experts is not None and (
+                experts.dtype != torch.uint8 or experts.device != self.weights.device or not experts.is_contiguous()
+                or experts.numel() < lib.dg_fp8_experts_bytes(ctypes.byref(self.cfg))):
+            raise ValueError("experts: a uint8 tensor from quantize_experts of the same configuration and device is needed")
+        n = lib.dg_fp8_experts_scratch_bytes(self.ctx)
+        if experts is not None and self.scratch8 is None:
+            # kept for the model's life, like the workspace
+            self.scratch8 = torch.empty(n, dtype=torch.uint8, device=self.weights.device)
+        if experts is not self.experts8:
+            torch.cuda.synchronize(self.weights.device)
+        check(lib.dg_fp8_experts_use(self.ctx, _ptr(experts), _ptr(self.scratch8), n))
+        self.experts8 = experts   # keeps them alive
 
     def encode(self, kv: KVCache, tokens: torch.Tensor, stream=None):
         assert tokens.dtype == torch.int32 and tokens.is_contiguous()

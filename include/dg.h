@@ -458,7 +458,9 @@ dg_status dg_fp8_grouped_gemm(const uint8_t* d_a, int64_t lda, const float* d_a_
    dg_fp8_experts_use switches the context to it (NULL: back to bf16) with a
    scratch buffer of dg_fp8_experts_scratch_bytes(ctx) bytes of its own, like
    the workspace: calls on one context must not overlap on the GPU.  Host-side
-   only; it drops the context's captured graph. */
+   only; it drops the context's captured graph.  Passes enqueued before the
+   switch go on reading and writing the old buffers: free or reuse those when
+   such passes have ended. */
 size_t dg_fp8_experts_bytes(const dg_model_config* cfg);
 size_t dg_fp8_experts_scratch_bytes(const dg_ctx* ctx);
 dg_status dg_fp8_experts_quantize(const dg_ctx* ctx, void* d_experts, size_t bytes, void* stream);

@@ -212,6 +212,42 @@ def test_experts_quantised_on_another_stream_are_its_memory():
     model.close()
 
 
+@pytest.mark.parametrize("to_bf16", [True, False], ids=["back to bf16", "to other matrices"])
+def test_a_switch_does_not_touch_the_work_before_it(to_bf16):
+    """A round enqueued on a side stream keeps its matrices and scratch, whatever is
+    allocated after the switch; so do the rounds after it."""
+    import discrete_diffusion_moe_b200 as dg
+    cfg = dg.model_config(**TINY)
+    model = dg.Model(cfg, 1, seed=0)
+    n = dg.lib.dg_fp8_experts_scratch_bytes(model.ctx)
+    kv, cv, out = dg.KVCache(cfg, 1, 512), dg.Canvas(cfg, 1), dg.StepOutputs(cfg, 1, logits=True)
+
+    def step(stream):
+        model.canvas_init(cv, 0, 7, stream=stream)
+        model.step(kv, cv, 0, 0, dg.sampler_config(seed=7, max_steps=2), out, stream=stream)
+    model.use_fp8_experts(model.quantize_experts())
+    step(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    want = out.logits.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    _busy(side)
+    step(side)
+    other = None if to_bf16 else model.quantize_experts()
+    model.use_fp8_experts(other)
+    size = dg.lib.dg_fp8_experts_bytes(ctypes.byref(cfg))
+    new = [torch.full((k,), 0x7F, dtype=torch.uint8, device="cuda") for k in (n, size, n, size)]
+    torch.cuda.synchronize()
+    assert torch.equal(out.logits, want)
+    if not to_bf16:
+        out.logits.zero_()
+        step(torch.cuda.current_stream())
+        assert torch.equal(out.logits, want)
+    assert all(bool((t == 0x7F).all()) for t in new)
+    model.check_device()
+    model.close()
+
+
 def test_refusals():
     import discrete_diffusion_moe_b200 as dg
     cfg = dg.model_config(**TINY)
