@@ -7,6 +7,8 @@ scale [(G,) ceil(N / 128), ceil(K / 128)]); a value is code * scale.  Rows of
 codes start every multiple of 16 bytes, so for other K the codes are a view
 of a wider buffer.  Tensors are on one CUDA device, which need not be the
 current one; work goes to `stream` (the device's current stream by default).
+That the inputs are ready on a given stream is the caller's part; that their
+memory is not given away before the work has ended is seen to here.
 Wrong shapes, types or strides raise ValueError, what the library itself
 refuses raises DgError; nothing is launched then."""
 
@@ -27,9 +29,9 @@ def _blocks(n):
     return (n + 127) >> 7
 
 
-def _launch(fn, device, stream, args):
-    """One library call on `device` and `stream` (its current one for None).
-    These calls take a few microseconds on the GPU, so the host side keeps to
+def _launch(fn, device, stream, args, tensors):
+    """One library call on `device` and `stream` (its current one for None),
+    which the memory of `tensors` (None among them) outlives.  These calls take a few microseconds on the GPU, so the host side keeps to
     plain integers: the raw stream and the current device's number."""
     index = device.index
     if stream is None:
@@ -37,6 +39,9 @@ def _launch(fn, device, stream, args):
     else:
         stream.device == device or _fail("the stream is on another device than the tensors")
         raw = stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, raw)
     else:
@@ -125,7 +130,7 @@ def fp8_quantize(x, index=None, act=None, out=None, stream=None):
         lds = _row_scale_pitch("out[1]", scale, device, rows, KB)
     _launch(lib.dg_fp8_quantize, device, stream,
             (x.data_ptr(), dtype, ldx if x_rows > 1 else cols, x_rows, index_ptr, _ACT[act], rows, K, q.data_ptr(),
-             q.stride(0) if rows > 1 else (K + 15) & ~15, scale.data_ptr(), lds))
+             q.stride(0) if rows > 1 else (K + 15) & ~15, scale.data_ptr(), lds), (x, index, q, scale))
     return q, scale
 
 
@@ -166,7 +171,7 @@ def fp8_quantize_blocks(w, out=None, stream=None):
     ldw, ldq = _weight_pitch("w", w), _weight_pitch("out[0]", q)
     _launch(lib.dg_fp8_quantize_blocks, w.device, stream,
             (w.data_ptr(), dtype, K if ldw is None else ldw, G, N, K, q.data_ptr(),
-             (K + 15) & ~15 if ldq is None else ldq, scale.data_ptr()))
+             (K + 15) & ~15 if ldq is None else ldq, scale.data_ptr()), (w, q, scale))
     return q, scale
 
 
@@ -206,13 +211,13 @@ def _product(a, a_scale, b, b_scale, off, row_weight, out_dtype, out, stream):
     if off is None:
         _launch(lib.dg_fp8_gemm, device, stream,
                 (a.data_ptr(), lda, a_scale.data_ptr(), lds, b.data_ptr(), ldb, b_scale.data_ptr(), M, N, K, weight_ptr,
-                 out.data_ptr(), dtype, ldo))
+                 out.data_ptr(), dtype, ldo), (a, a_scale, b, b_scale, row_weight, out))
     else:
         G = shape[0]
         _check_vector("off", off, device, torch.int32, G + 1)
         _launch(lib.dg_fp8_grouped_gemm, device, stream,
                 (a.data_ptr(), lda, a_scale.data_ptr(), lds, b.data_ptr(), ldb, b_scale.data_ptr(), off.data_ptr(), G, M, N,
-                 K, weight_ptr, out.data_ptr(), dtype, ldo))
+                 K, weight_ptr, out.data_ptr(), dtype, ldo), (a, a_scale, b, b_scale, off, row_weight, out))
     return out
 
 

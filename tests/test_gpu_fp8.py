@@ -570,6 +570,41 @@ def test_given_stream():
     assert torch.equal(q.view(torch.uint8), dg.fp8_quantize(want)[0].view(torch.uint8))
 
 
+def test_given_stream_keeps_its_inputs():
+    """Inputs (and outputs) that the caller lets go while a busy stream has yet to
+    read them are not given to other tensors."""
+    dg = _dg()
+    rng = np.random.default_rng(10)
+    M, N, K, G = 300, 256, 512, 2
+    a, sa = ref.random_operand(rng, M, K)
+    b, sb = ref.random_weights(rng, N, K, G=G)
+    inputs = dict(x=torch.randn(M, K, device="cuda").to(torch.bfloat16),
+                  index=torch.from_numpy(rng.permutation(M).astype(np.int32)).cuda(),
+                  w=torch.randn(G, N, K, device="cuda"), a=a, sa=sa, b=b, sb=sb, rw=torch.rand(M, device="cuda"),
+                  off=torch.tensor([0, 100, M], dtype=torch.int32, device="cuda"))
+
+    def calls(i, stream):
+        return (*dg.fp8_quantize(i["x"], index=i["index"], stream=stream), *dg.fp8_quantize_blocks(i["w"], stream=stream),
+                dg.fp8_gemm(i["a"], i["sa"], i["b"][1], i["sb"][1], row_weight=i["rw"], stream=stream),
+                dg.fp8_grouped_gemm(i["a"], i["sa"], i["b"], i["sb"], i["off"], row_weight=i["rw"], stream=stream))
+    want = calls(inputs, None)
+    side = torch.cuda.Stream()
+    mine = {k: t.view(torch.uint8).clone().view(t.dtype) if t.dtype == torch.float8_e4m3fn else t.clone()
+            for k, t in inputs.items()}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    at = {t.untyped_storage().data_ptr() for t in mine.values()}
+    sizes = [t.untyped_storage().nbytes() for t in mine.values()]
+    got = calls(mine, side)
+    del mine
+    new = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    assert not at & {t.untyped_storage().data_ptr() for t in new}
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def _held(dg, what, unit, block, call):
     """`call` with something left out of one unit of its kernel, so that waits run out."""
     dg.check(dg.lib.dg_test_fp8_hold(what, unit, block, 20_000_000))
