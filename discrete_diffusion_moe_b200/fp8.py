@@ -10,7 +10,8 @@ current one; work goes to `stream` (the device's current stream by default).
 That the inputs are ready on a given stream is the caller's part; that their
 memory is not given away before the work has ended is seen to here.
 Wrong shapes, types or strides raise ValueError, what the library itself
-refuses raises DgError; nothing is launched then."""
+refuses raises DgError; nothing is launched then.  No gradients flow through
+these calls."""
 
 import torch
 

@@ -412,6 +412,38 @@ def test_offsets_beyond_32_bits():
             row += n
 
 
+def test_quantised_offsets_beyond_32_bits():
+    """Inputs and codes of more than 2^32 bytes: the last rows and blocks."""
+    dg = _dg()
+    rows, K = 70003, 65544   # K ends inside a block
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda").normal_()
+    q, s = dg.fp8_quantize(x)
+    assert q.numel() > 2 ** 32
+    last = x[-2:].double().cpu().numpy()
+    want_q, want_s = ref.quantize_rows(last)
+    _same_codes(q[-2:], want_q)
+    _same_scales(s[:, -2:], want_s)
+    del q, s
+    q, s = dg.fp8_quantize(x, index=torch.tensor([rows - 1, rows, rows - 2, rows - 1], dtype=torch.int32, device="cuda"))
+    for r, w in ((0, 1), (2, 0), (3, 1)):
+        _same_codes(q[r:r + 1], want_q[w:w + 1])
+        _same_scales(s[:, r:r + 1], want_s[:, w:w + 1])
+    assert not q[1].float().any()
+    y, sy = dg.fp8_quantize(x, act="swiglu")
+    halves = ref.swiglu(last[:, :K // 2], last[:, K // 2:])
+    got = ref.dequantize_rows(y[-2:], sy[:, -2:])
+    step = np.repeat(sy[:, -2:].double().cpu().numpy().T, 128, axis=1)[:, :K // 2]
+    assert np.all(np.abs(got - halves) <= (2.0 ** -4 + 2.0 ** -19) * np.abs(halves) + 2.0 ** -10 * step)
+    del y, sy
+    w = x[:70000].view(2, 35000, K)
+    q, s = dg.fp8_quantize_blocks(w)
+    assert q.numel() > 2 ** 32
+    r0 = 35000 // 128 * 128
+    want_q, want_s = ref.quantize_blocks(w[1, r0:, -264:].double().cpu().numpy())   # from a block's first row and column
+    _same_codes(q[1, r0:, -264:], want_q)
+    _same_scales(s[1, -1:, -3:], want_s)
+
+
 def _in_range(got, want, want_abs, K):
     """The results without those outside got's type.  A value is rounded to an infinity from
     half a step above the largest finite one on (fp16: 65504 + 16); within the bound's
@@ -603,6 +635,27 @@ def test_given_stream_keeps_its_inputs():
     torch.cuda.synchronize()
     for x, y in zip(got, want):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_captured_on_a_given_stream():
+    """A graph of calls that name the stream they are captured on, replayed on new inputs."""
+    dg = _dg()
+    rng = np.random.default_rng(11)
+    b, sb = ref.random_weights(rng, 192, 256)
+    x = torch.randn(70, 256, device="cuda").to(torch.bfloat16)
+
+    def block(stream):
+        return dg.fp8_gemm(*dg.fp8_quantize(x, stream=stream), b, sb, stream=stream)
+    want = block(None).clone()
+    torch.cuda.synchronize()
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        out = block(st)
+    for factor in (1.0, -2.0):
+        x.mul_(factor)
+        g.replay()
+        assert torch.equal(out, block(None))
+    assert torch.equal(out, -2.0 * want)   # a power of two scales every step exactly
 
 
 def _held(dg, what, unit, block, call):
