@@ -13,9 +13,11 @@
 // so lane (g, t) of a warp takes bytes [16 t, 16 t + 16) of both halves of its
 // rows' 128: two 16-byte loads per row, each of whole sectors, and four products
 // per block.  The eight warps of a CTA share its 16 features and take every
-// eighth block of K each.  One block per warp is in flight, and 48 registers let
-// five CTAs share an SM: with three blocks in flight and two CTAs 5632 features
-// of one token took 7.7 us (two waves), so 6.6; 8 experts 14.0, so 10.4.  The
+// eighth block of K each.  One block per warp is in flight, so the 22 blocks of K = 2816
+// are three trips to HBM one after another; 48 registers let five CTAs share an SM (at
+// the price of 48 bytes of spill stores and 44 of loads).  With three blocks in flight
+// and two CTAs 5632 features of one token took 7.7 us (two waves), so 6.3; 8 experts
+// 14.0, so 10.3.  The
 // warps' fp32 sums meet in shared memory in the order of the warps (the result
 // does not depend on timing).
 #pragma once
