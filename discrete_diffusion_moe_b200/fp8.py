@@ -32,8 +32,9 @@ def _blocks(n):
 
 def _launch(fn, device, stream, args, tensors):
     """One library call on `device` and `stream` (its current one for None),
-    which the memory of `tensors` (None among them) outlives.  These calls take a few microseconds on the GPU, so the host side keeps to
-    plain integers: the raw stream and the current device's number."""
+    which the memory of `tensors` (None among them) outlives.  These calls take
+    a few microseconds on the GPU, so the host side keeps to plain integers:
+    the raw stream and the current device's number."""
     index = device.index
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
