@@ -140,6 +140,21 @@ def test_quantize_swiglu_is_as_exact_as_fp32_allows(act):
     assert np.array_equal(q.double().cpu().numpy()[:, 0], 448 * np.sign(gd))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_swiglu_of_the_largest_gates(dtype):
+    """Gates of the type's largest magnitude with small factors: silu is the gate itself, or
+    0 for negative ones (a block of zeros has the smallest scale).  The scale is within 5
+    units of 2^-23."""
+    dg = _dg()
+    big = torch.finfo(dtype).max
+    x = torch.tensor([[big, 2.0 ** -20], [-big, 2.0 ** -20], [big / 2, -2.0 ** -14]], dtype=dtype)
+    q, s = dg.fp8_quantize(x.cuda(), act="swiglu")
+    d = x.double().numpy()
+    want = np.maximum(np.abs(np.where(d[:, 0] > 0, d[:, 0], 0.0) * d[:, 1]), ref.AMAX_MIN) / 448
+    assert np.all(np.abs(s[0].double().cpu().numpy() / want - 1) <= 5 * 2.0 ** -23)
+    assert q.double().cpu().numpy()[:, 0].tolist() == [448.0, 0.0, -448.0]
+
+
 @pytest.mark.parametrize("act", ["swiglu", "swiglu_interleaved"])
 def test_quantize_swiglu_special_values(act):
     """Gates of either infinity and far from zero, NaN gates and values: the
